@@ -309,10 +309,12 @@ def _prepare_prefix(case, g):
                  block_table=order[np_:].reshape(B, ns).to(torch.int32).contiguous())
     if own:
         import bit_quantized_attention_qk4v8_b200 as qk
-        s["packed_q"] = qk.MXFP4(s["q"], s["qs"], B, H * G, 128, nq)
+        s["packed_q"] = qk.MXFP4(s["q"].contiguous(), s["qs"].contiguous(), B, H * G, 128, nq)
         if case["paged"]:
             s["cache"] = qk.PagedKV(s["pk"], s["pks"], s["pv"], s["pvs"], None, s["block_table"], lens)
         else:
+            # The packed buffers of a program are dense; the ones made above may be permuted views.
+            kp, ksp, vp, vsp, k, ks, v, vs = (a.contiguous() for a in (kp, ksp, vp, vsp, k, ks, v, vs))
             s["prefix_kv"] = (qk.MXFP4(kp, ksp, 1, H, _cap(prefix), prefix), qk.MXFP8V(vp, vsp, 1, H, _cap(prefix), prefix))
             s["own_kv"] = (qk.MXFP4(k, ks, B, H, _cap(suffix), suffix), qk.MXFP8V(v, vs, B, H, _cap(suffix), suffix))
     return s
