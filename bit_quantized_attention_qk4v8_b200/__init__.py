@@ -13,13 +13,14 @@ Method (MpFA QK4V8 article, mhpn.cn):
 """
 from __future__ import annotations
 
+import ctypes
 import math
-from dataclasses import dataclass
-from typing import Optional
+from dataclasses import dataclass, field
+from typing import Optional, Sequence
 
 import torch
 
-from ._lib import QK4V8Error, check, lib
+from ._lib import QK4V8Error, RopeStruct, check, lib
 
 __all__ = [
     "MXFP4", "MXFP4V", "MXFP8V", "PagedKV", "QK4V8Error", "lib", "round_cap",
@@ -28,6 +29,9 @@ __all__ = [
     "decode_merge",
     "attention_decode_bf16", "decode_bf16_workspace_bytes",
     "paged_kv", "kv_append", "attention_decode_paged", "attention_decode_bf16_paged", "quantize_v4",
+    "Rope", "rope_table", "quantize_qk_rope", "kv_append_rope",
+    "attention_decode_prefix", "attention_decode_prefix_paged", "decode_prefix_default_splits",
+    "decode_prefix_workspace_bytes",
 ]
 
 D = 128
@@ -485,4 +489,248 @@ def attention_decode_bf16_paged(q: torch.Tensor, cache: PagedKV, max_seqlen: int
                                                   float(softmax_scale or 0.0), int(splits), _ptr(workspace), ws_bytes,
                                                   out.data_ptr(), _ptr(lse), _ptr(dev_status), _stream(dev)),
           "qk4v8_attention_decode_bf16_paged")
+    return (out, lse) if return_lse else out
+
+
+def _check_dense(device, *tensors):
+    for t in tensors:
+        if t.device != device or not t.is_contiguous():
+            raise ValueError("packed buffers must be contiguous and on one device")
+
+
+# ----------------------------------------------------------------------------------------------------------
+# Rotary positions (include/qk4v8.h: qk4v8_rope, qk4v8_quantize_qk_rope, qk4v8_kv_append_rope).
+
+@dataclass
+class Rope:
+    """A model's rotary positions: what a program makes once and gives to every call.
+
+    table float32 [max_pos, rotary_dim / 2, 2] (CUDA, contiguous): cosine and sine of
+    position p for pair i (rope_table makes the usual one); adjacent: pairs (2i, 2i + 1)
+    instead of (i, i + rotary_dim / 2); pair_axis: axis of each pair (rotary_dim / 2
+    entries of 0..3) when positions have several axes."""
+    table: torch.Tensor
+    adjacent: bool = False
+    pair_axis: Optional[Sequence[int]] = None
+    n_axes: int = field(init=False)
+    _axes: object = field(init=False, repr=False)
+
+    def __post_init__(self):
+        t = self.table
+        if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 3 or t.shape[2] != 2 or not t.is_contiguous():
+            raise ValueError("table must be a contiguous CUDA float32 tensor [max_pos, rotary_dim / 2, 2]")
+        self._axes, self.n_axes = None, 1
+        if self.pair_axis is not None:
+            axes = [int(a) for a in self.pair_axis]
+            if len(axes) != t.shape[1] or min(axes) < 0 or max(axes) > 3:
+                raise ValueError("pair_axis must have rotary_dim / 2 entries of 0..3")
+            self._axes, self.n_axes = (ctypes.c_uint8 * len(axes))(*axes), max(axes) + 1
+
+    @property
+    def rotary_dim(self) -> int:
+        return 2 * self.table.shape[1]
+
+
+def rope_table(max_pos: int, rotary_dim: int = D, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Rope.table with angles p * base^(-2 i / rotary_dim), taken in fp64 (far positions) and held in fp32."""
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    p = torch.arange(max_pos, dtype=torch.float64, device=device)
+    angle = p[:, None] * (float(base) ** (-2.0 * i / rotary_dim))
+    return torch.stack((angle.cos(), angle.sin()), -1).to(torch.float32).contiguous()
+
+
+def _rope_struct(rope: Rope, positions: Optional[torch.Tensor], B: int, T: int, device) -> RopeStruct:
+    if rope.table.device != device:
+        raise ValueError("rope.table must be on the inputs' device")
+    s = RopeStruct(rope.table.data_ptr(), rope.table.shape[0], 2 * rope.table.shape[1], int(rope.adjacent),
+                   rope.n_axes, None if rope._axes is None else ctypes.addressof(rope._axes))
+    if positions is not None:
+        if positions.dim() == 2:
+            positions = positions.unsqueeze(0)
+        if positions.dtype != torch.int32 or positions.device != device or positions.dim() != 3 or \
+                positions.shape[0] < rope.n_axes or tuple(positions.shape[1:]) != (B, T):
+            raise ValueError("positions must be an int32 tensor [B, T] or [axes, B, T] on the inputs' device, with an "
+                             "axis for each one that rope.pair_axis names")
+        s.positions = positions.data_ptr()
+        s.pos_stride_axis, s.pos_stride_b, s.pos_stride_t = positions.stride()
+    return s
+
+
+def _int32_on(t: Optional[torch.Tensor], B: int, device, name: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != (B,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on the inputs' device")
+    return t.data_ptr()
+
+
+def quantize_qk_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tensor] = None,
+                     start: Optional[torch.Tensor] = None, cap: Optional[int] = None, seqlens=None,
+                     out: Optional[MXFP4] = None, hadamard: bool = False, pad: bool = True,
+                     dev_status: Optional[torch.Tensor] = None) -> MXFP4:
+    """Rotate Q or K ([B, T, H, 128] bf16) by their positions and MXFP4-quantize them, in one pass
+    (qk4v8_quantize_qk_rope).
+
+    positions: int32 [B, T] or [axes, B, T], any strides (an expanded one is read in place); without them
+    token t of sequence b is at start[b] + t (start: int32 [B], None: 0). pad=False writes the T given rows
+    and leaves the rest of `out` (a buffer kept over the decode steps) as it is."""
+    _check_bf16(x, "x")
+    B, T, H, _ = x.shape
+    dev = x.device
+    if out is not None:
+        if out.B != B or out.H != H or (cap is not None and cap != out.cap):
+            raise ValueError("out must be a packed tensor of the same B, H and capacity")
+        _check_dense(dev, out.codes, out.scales)
+        cap = out.cap
+    elif cap is None:
+        cap = round_cap(T)
+    sl = _seqlens(seqlens, B, dev)
+    rs = _rope_struct(rope, positions, B, T, dev)
+    st = _int32_on(start, B, dev, "start")
+    if out is None:
+        out = MXFP4(torch.empty((B, H, cap, 64), dtype=torch.uint8, device=dev),
+                    torch.empty((B, H, cap // 128, 512), dtype=torch.uint8, device=dev), B, H, cap, T)
+    with torch.cuda.device(dev):
+        check(lib().qk4v8_quantize_qk_rope(x.data_ptr(), B, T, H, D, x.stride(0), x.stride(1), x.stride(2), _ptr(sl), st,
+                                           ctypes.addressof(rs), int(bool(hadamard)), cap, int(bool(pad)),
+                                           out.codes.data_ptr(), out.scales.data_ptr(), _ptr(dev_status),
+                                           _stream(dev)), "qk4v8_quantize_qk_rope")
+    out.length = T
+    return out
+
+
+def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rope: Rope,
+                   positions: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                   seqlens_out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None) -> PagedKV:
+    """Append k_new (rotated by its positions) and v_new (bf16 [B, n_new, Hkv, 128], strides of their own) to the
+    sequences (qk4v8_kv_append_rope).
+
+    new_lens: int32 [B], the sequence's first new_lens[b] tokens are appended (None: all n_new).
+    positions as for quantize_qk_rope; without them a token is at its place in the sequence.
+    cache.seqlens advances on the device, unless seqlens_out (int32 [B]) receives the new lengths."""
+    _check_bf16(k_new, "k_new")
+    _check_bf16(v_new, "v_new")
+    B, n_new, Hkv, _ = k_new.shape
+    dev = k_new.device
+    if v_new.shape != k_new.shape or v_new.device != dev:
+        raise ValueError("k_new and v_new must have the same shape and device")
+    if B != cache.B or Hkv != cache.Hkv:
+        raise ValueError("k_new must be [cache.B, n_new, cache.Hkv, 128]")
+    _check_dense(dev, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, cache.v_tail, cache.block_table,
+                 cache.seqlens)
+    rs = _rope_struct(rope, positions, B, n_new, dev)
+    nl = _int32_on(new_lens, B, dev, "new_lens")
+    lens = cache.seqlens.data_ptr()
+    so = lens if seqlens_out is None else _int32_on(seqlens_out, B, dev, "seqlens_out")
+    strides = ctypes.c_int64 * 3
+    ks, vs = strides(*k_new.stride()[:3]), strides(*v_new.stride()[:3])
+    with torch.cuda.device(dev):
+        check(lib().qk4v8_kv_append_rope(k_new.data_ptr(), v_new.data_ptr(), B, n_new, Hkv, D, ctypes.addressof(ks),
+                                         ctypes.addressof(vs), lens, nl, so, ctypes.addressof(rs),
+                                         cache.block_table.data_ptr(), cache.max_pages, cache.num_pages,
+                                         cache.k_codes.data_ptr(), cache.k_scales.data_ptr(),
+                                         cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), cache.v_tail.data_ptr(),
+                                         int(cache.hadamard_k), _ptr(dev_status), _stream(dev)),
+              "qk4v8_kv_append_rope")
+    return cache
+
+
+# ----------------------------------------------------------------------------------------------------------
+# Decode over a shared prefix (include/qk4v8.h: qk4v8_attention_decode_prefix).
+
+def decode_prefix_workspace_bytes(B: int, Hq: int, nq: int, prefix_splits: int, num_splits: int) -> int:
+    return int(lib().qk4v8_decode_prefix_workspace_bytes(B, Hq, nq, prefix_splits, num_splits))
+
+
+def decode_prefix_default_splits(B: int, Hq: int, Hkv: int, nq: int, prefix_len: int) -> int:
+    return int(lib().qk4v8_decode_prefix_default_splits(B, Hq, Hkv, nq, prefix_len))
+
+
+def _prefix_buffers(q: MXFP4, Hkv: int, prefix_len: int, max_seqlen: int, prefix_splits: int, num_splits: int,
+                    workspace, out, lse, return_lse):
+    dev = q.codes.device
+    B, Hq, nq = q.B, q.H, q.length
+    tiles = (prefix_len + 127) // 128
+    if tiles == 0:
+        ps = 0
+    elif prefix_splits > 0:
+        ps = min(prefix_splits, tiles)
+    else:
+        ps = decode_prefix_default_splits(B, Hq, Hkv, nq, prefix_len)
+    if max_seqlen == 0:
+        ns = 0
+    else:
+        ns = num_splits if num_splits > 0 else decode_default_splits(B, Hq, Hkv, nq, max_seqlen)
+    if workspace is None:
+        workspace = torch.empty((max(16, decode_prefix_workspace_bytes(B, Hq, nq, ps, ns)),), dtype=torch.uint8,
+                                device=dev)
+    if out is None:
+        out = torch.empty((B, nq, Hq, D), dtype=torch.bfloat16, device=dev)
+    if return_lse and lse is None:
+        lse = torch.empty((B, Hq, nq), dtype=torch.float32, device=dev)
+    return ps, ns, workspace, workspace.numel() * workspace.element_size(), out, lse
+
+
+def attention_decode_prefix(q: MXFP4, k_prefix: MXFP4, v_prefix: MXFP8V, k: MXFP4, v: MXFP8V, seqlens_k,
+                            max_seqlen: Optional[int] = None, prefix_len: Optional[int] = None,
+                            causal_in_block: bool = True, softmax_scale: Optional[float] = None,
+                            prefix_splits: int = 0, num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            return_lse: bool = False, dev_status: Optional[torch.Tensor] = None):
+    """Decode / verify of sequences that share a prefix (k_prefix, v_prefix: packed with B = 1), followed by their
+    own keys (k, v, seqlens_k as for attention_decode; a length may be 0). The prefix is read once for all
+    (qk4v8_attention_decode_prefix). Returns out bf16 [B, nq, Hq, 128] (and lse [B, Hq, nq])."""
+    dev = q.codes.device
+    B, Hq, nq = q.B, q.H, q.length
+    if k_prefix.B != 1 or v_prefix.B != 1 or k_prefix.H != k.H or v_prefix.H != k.H or k_prefix.cap != v_prefix.cap:
+        raise ValueError("k_prefix and v_prefix must be packed tensors with B = 1, the KV heads of k and one capacity")
+    if k.B != B or v.B != B or v.H != k.H or k.cap != v.cap:
+        raise ValueError("k and v must be packed tensors of q's batch with the same heads and capacity")
+    if not isinstance(v, MXFP8V) or not isinstance(v_prefix, MXFP8V):
+        raise ValueError("v and v_prefix must be MXFP8 (MXFP8V)")
+    _check_dense(dev, q.codes, q.scales, k_prefix.codes, k_prefix.scales, v_prefix.codes, v_prefix.scales, k.codes,
+                 k.scales, v.codes, v.scales)
+    prefix_len = k_prefix.length if prefix_len is None else int(prefix_len)
+    max_seqlen = k.cap if max_seqlen is None else int(max_seqlen)
+    sl = _seqlens(seqlens_k, B, dev)
+    ps, ns, ws, ws_bytes, out, lse = _prefix_buffers(q, k.H, prefix_len, max_seqlen, prefix_splits, num_splits,
+                                                     workspace, out, lse, return_lse)
+    with torch.cuda.device(dev):
+        check(lib().qk4v8_attention_decode_prefix(
+            q.codes.data_ptr(), q.scales.data_ptr(), B, Hq, nq, q.cap, k_prefix.codes.data_ptr(),
+            k_prefix.scales.data_ptr(), v_prefix.codes.data_ptr(), v_prefix.scales.data_ptr(), prefix_len, k_prefix.cap,
+            k.codes.data_ptr(), k.scales.data_ptr(), v.codes.data_ptr(), v.scales.data_ptr(), k.H, k.cap, _ptr(sl),
+            max_seqlen, int(bool(causal_in_block)), float(softmax_scale or 0.0), ps, ns, ws.data_ptr(), ws_bytes,
+            out.data_ptr(), _ptr(lse), _ptr(dev_status), _stream(dev)), "qk4v8_attention_decode_prefix")
+    return (out, lse) if return_lse else out
+
+
+def attention_decode_prefix_paged(q: MXFP4, cache: PagedKV, prefix_table: torch.Tensor, prefix_len: int,
+                                  max_seqlen: int, causal_in_block: bool = True,
+                                  softmax_scale: Optional[float] = None, prefix_splits: int = 0, num_splits: int = 0,
+                                  workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                  lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                                  dev_status: Optional[torch.Tensor] = None):
+    """attention_decode_prefix over a page pool: prefix_table int32 [pages] lists the prefix's pages, the cache's
+    block_table and seqlens hold the sequences' own tokens (qk4v8_attention_decode_prefix_paged)."""
+    dev = q.codes.device
+    B, Hq, nq = q.B, q.H, q.length
+    prefix_len, max_seqlen = int(prefix_len), int(max_seqlen)
+    if cache.B != B:
+        raise ValueError("the cache must hold q's batch")
+    _check_dense(dev, q.codes, q.scales, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales,
+                 cache.block_table, cache.seqlens)
+    if prefix_table.dtype != torch.int32 or prefix_table.device != dev or prefix_table.dim() != 1 or \
+            not prefix_table.is_contiguous() or prefix_table.shape[0] * 128 < prefix_len:
+        raise ValueError("prefix_table must be a contiguous int32 tensor of the prefix's pages on q's device")
+    ps, ns, ws, ws_bytes, out, lse = _prefix_buffers(q, cache.Hkv, prefix_len, max_seqlen, prefix_splits, num_splits,
+                                                     workspace, out, lse, return_lse)
+    with torch.cuda.device(dev):
+        check(lib().qk4v8_attention_decode_prefix_paged(
+            q.codes.data_ptr(), q.scales.data_ptr(), B, Hq, nq, q.cap, cache.k_codes.data_ptr(),
+            cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), cache.Hkv, cache.num_pages,
+            prefix_table.data_ptr(), prefix_len, cache.block_table.data_ptr(), cache.max_pages,
+            cache.seqlens.data_ptr(), max_seqlen, int(bool(causal_in_block)), float(softmax_scale or 0.0), ps, ns,
+            ws.data_ptr(), ws_bytes, out.data_ptr(), _ptr(lse), _ptr(dev_status), _stream(dev)),
+            "qk4v8_attention_decode_prefix_paged")
     return (out, lse) if return_lse else out

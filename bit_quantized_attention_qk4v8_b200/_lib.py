@@ -15,6 +15,15 @@ _lib = None
 
 # Every exported entry point, with ctypes signatures (argtypes, restype).
 _vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+
+
+class RopeStruct(ctypes.Structure):
+    """qk4v8_rope of include/qk4v8.h."""
+    _fields_ = [("table", _vp), ("max_pos", _i32), ("rotary_dim", _i32), ("adjacent", _i32), ("n_axes", _i32),
+                ("pair_axis", _vp), ("positions", _vp), ("pos_stride_axis", _i64), ("pos_stride_b", _i64),
+                ("pos_stride_t", _i64)]
+
+
 SIGNATURES = {
     "qk4v8_status_string": ([_i32], ctypes.c_char_p),
     "qk4v8_last_error": ([], ctypes.c_char_p),
@@ -58,6 +67,18 @@ SIGNATURES = {
     "qk4v8_attention_decode_bf16_paged": ([_vp, _i32, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i32,
                                            _vp, _i32, _vp, _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp, _vp, _vp,
                                            _vp], _i32),
+    "qk4v8_quantize_qk_rope": ([_vp, _i32, _i32, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp,
+                                _vp, _vp, _vp], _i32),
+    "qk4v8_kv_append_rope": ([_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp,
+                              _vp, _vp, _vp, _vp, _i32, _vp, _vp], _i32),
+    "qk4v8_decode_prefix_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32], _sz),
+    "qk4v8_decode_prefix_default_splits": ([_i32, _i32, _i32, _i32, _i32], _i32),
+    "qk4v8_attention_decode_prefix": ([_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp,
+                                       _vp, _vp, _i32, _i32, _vp, _i32, _i32, _f32, _i32, _i32, _vp, _sz, _vp, _vp,
+                                       _vp, _vp], _i32),
+    "qk4v8_attention_decode_prefix_paged": ([_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp,
+                                             _i32, _vp, _i32, _vp, _i32, _i32, _f32, _i32, _i32, _vp, _sz, _vp, _vp,
+                                             _vp, _vp], _i32),
     "qk4v8_decode_bf16_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32], _sz),
     "qk4v8_attention_decode_bf16": ([_vp, _i32, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _vp,
                                      _i32, _i32, _f32, _i32, _vp, _sz, _vp, _vp, _vp, _vp], _i32),

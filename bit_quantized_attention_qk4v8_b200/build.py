@@ -10,9 +10,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqk4v8.so")
-SOURCES = ["quantize.cu", "attention.cu", "prefill.cu", "decode.cu", "gqa_decode.cu", "mma_peak.cu", "kv_cache.cu",
+SOURCES = ["quantize.cu", "attention.cu", "prefill.cu", "decode.cu", "gqa_decode.cu", "mma_peak.cu", "kv_cache.cu", "rope.cu", "prefix.cu",
            "api.cu"]
-HEADERS = ["ptx.cuh", "pipeline.cuh", "mx_encode.cuh", "tile_ops.cuh", "schedule.cuh", "qk4v8_internal.h"]
+HEADERS = ["ptx.cuh", "pipeline.cuh", "mx_encode.cuh", "rope.cuh", "tile_ops.cuh", "schedule.cuh", "qk4v8_internal.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

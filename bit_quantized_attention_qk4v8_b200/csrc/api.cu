@@ -1047,3 +1047,277 @@ int qk4v8_attention_decode_noalloc(const uint8_t *q_codes, const uint8_t *q_scal
 }
 
 }  // extern "C"
+
+namespace {
+
+// Checks a caller's rotary description and turns it into the kernels' form.
+int resolve_rope(const qk4v8_rope *r, qk4v8::RopeParams *out) {
+    if (!r || !r->table || !aligned16(r->table))
+        return set_error(QK4V8_ERR_INVALID_ARG, "rope needs a 16-byte aligned table");
+    if (r->max_pos <= 0 || r->rotary_dim <= 0 || r->rotary_dim > 128 || r->rotary_dim % 16)
+        return set_error(QK4V8_ERR_INVALID_ARG, "rope: max_pos must be positive and rotary_dim a multiple of 16 up to "
+                                                "128 (got %d, %d)", r->max_pos, r->rotary_dim);
+    if (r->n_axes < 1 || r->n_axes > 4)
+        return set_error(QK4V8_ERR_INVALID_ARG, "rope: 1 to 4 axes (got %d)", r->n_axes);
+    if (r->positions && (r->pos_stride_axis < 0 || r->pos_stride_b < 0 || r->pos_stride_t < 0))
+        return set_error(QK4V8_ERR_INVALID_ARG, "rope: position strides must not be negative");
+    *out = qk4v8::RopeParams{};
+    out->table = r->table;
+    out->max_pos = r->max_pos;
+    out->rotary = r->rotary_dim;
+    out->adjacent = r->adjacent ? 1 : 0;
+    // Without a pair of another axis, one axis (the kernels read its positions alone).
+    out->n_axes = 1;
+    if (r->pair_axis)
+        for (int i = 0; i < r->rotary_dim / 2; ++i) {
+            const unsigned a = r->pair_axis[i];
+            if (a >= static_cast<unsigned>(r->n_axes))
+                return set_error(QK4V8_ERR_INVALID_ARG, "rope: pair %d on axis %u of %d", i, a, r->n_axes);
+            out->pair_axis[i >> 5] |= static_cast<uint64_t>(a) << (2 * (i & 31));
+            if (a) out->n_axes = r->n_axes;
+        }
+    out->positions = r->positions;
+    out->pos_sa = r->pos_stride_axis;
+    out->pos_sb = r->pos_stride_b;
+    out->pos_st = r->pos_stride_t;
+    if (!r->positions) out->n_axes = 1;  // the token's index on every axis
+    return QK4V8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qk4v8_quantize_qk_rope(const void *x, int B, int S, int H, int d, int64_t stride_b, int64_t stride_s,
+                           int64_t stride_h, const int32_t *seqlens, const int32_t *start, const qk4v8_rope *rope,
+                           int hadamard, int cap, int pad, uint8_t *codes, uint8_t *scales, int32_t *dev_status,
+                           void *stream) {
+    int st = validate_quant_args(x, B, S, H, d, stride_b, stride_s, stride_h, cap, codes, scales);
+    if (st) return st;
+    qk4v8::RopeParams r;
+    if ((st = resolve_rope(rope, &r))) return st;
+    if ((st = check_device())) return st;
+    cudaError_t e = qk4v8::launch_quantize_qk_rope(x, B, S, H, stride_b, stride_s, stride_h, seqlens, start, cap, r,
+                                                   hadamard != 0, pad != 0, codes, scales, dev_status,
+                                                   static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QK4V8_OK : cuda_error(e, "quantize_qk_rope launch");
+}
+
+int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, int n_new, int Hkv, int d,
+                         const int64_t *k_strides, const int64_t *v_strides, const int32_t *seqlens,
+                         const int32_t *new_lens, int32_t *seqlens_out, const qk4v8_rope *rope,
+                         const int32_t *block_table, int max_pages, int num_pages, uint8_t *k_codes,
+                         uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales, void *v_tail, int hadamard_k,
+                         int32_t *dev_status, void *stream) {
+    if (!k_new || !v_new || !k_strides || !v_strides || !seqlens || !block_table || !k_codes || !k_scales ||
+        !v_codes || !v_scales || !v_tail)
+        return set_error(QK4V8_ERR_INVALID_ARG, "null pointer");
+    if (d != 128) return set_error(QK4V8_ERR_INVALID_ARG, "head_dim must be 128 (got %d)", d);
+    if (B <= 0 || n_new <= 0 || n_new >= (1 << 30) || Hkv <= 0 || max_pages <= 0 || max_pages >= (1 << 23) ||
+        num_pages <= 0 || static_cast<int64_t>(num_pages) * Hkv >= (int64_t{1} << 31))
+        return set_error(QK4V8_ERR_INVALID_ARG, "bad sizes B=%d n_new=%d Hkv=%d max_pages=%d num_pages=%d", B, n_new,
+                         Hkv, max_pages, num_pages);
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
+        !aligned16(v_scales) || !aligned16(v_tail))
+        return set_error(QK4V8_ERR_INVALID_ARG, "K/V inputs, pools and v_tail must be 16-byte aligned");
+    int64_t ks[3], vs[3];
+    for (int i = 0; i < 3; ++i) {
+        ks[i] = k_strides[i];
+        vs[i] = v_strides[i];
+        if (ks[i] % 8 || vs[i] % 8 || ks[i] < 0 || vs[i] < 0)
+            return set_error(QK4V8_ERR_INVALID_ARG, "strides must be non-negative multiples of 8 elements");
+    }
+    qk4v8::RopeParams r;
+    int st = resolve_rope(rope, &r);
+    if (st) return st;
+    if ((st = check_device())) return st;
+    cudaError_t e = qk4v8::launch_kv_append_rope(k_new, v_new, B, n_new, Hkv, ks, vs, seqlens, new_lens, seqlens_out,
+                                                 block_table, max_pages, num_pages, k_codes, k_scales, v_codes,
+                                                 v_scales, v_tail, r, hadamard_k != 0, dev_status,
+                                                 static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QK4V8_OK : cuda_error(e, "kv append (rope) launch");
+}
+
+size_t qk4v8_decode_prefix_workspace_bytes(int B, int Hq, int nq, int prefix_splits, int num_splits) {
+    if (B <= 0 || Hq <= 0 || nq <= 0 || prefix_splits < 0 || num_splits < 0) return 0;
+    // The prefix's partials and log2-sum-exp, then the split kernel's workspace.
+    const size_t rows = static_cast<size_t>(B) * Hq * nq * prefix_splits;
+    return (rows * 129 * sizeof(float) + 15) / 16 * 16 + qk4v8_decode_workspace_bytes(B, Hq, nq, num_splits);
+}
+
+int qk4v8_decode_prefix_default_splits(int B, int Hq, int Hkv, int nq, int prefix_len) {
+    // `rows` of 128 query rows times `s` splits of the prefix's key tiles run in waves of
+    // one CTA per SM, each as long as its tiles plus a fixed cost (start, first loads,
+    // epilogue) of about kOverheadTiles; every split adds a partial result to join.
+    constexpr int kOverheadTiles = 5, kMaxSplits = 148;
+    if (B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || nq <= 0 || prefix_len <= 0) return 1;
+    int sms = 148, dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+        sms = 148;
+        (void)cudaGetLastError();
+    }
+    const int64_t rows = static_cast<int64_t>(B) * (Hq / Hkv) * nq;
+    const int64_t units = (rows + 127) / 128 * Hkv;
+    const int tiles = (prefix_len + 127) / 128;
+    int best = 1;
+    int64_t best_cost = INT64_MAX;
+    for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
+        const int64_t waves = (units * s + sms - 1) / sms;
+        const int64_t cost = waves * ((tiles + s - 1) / s + kOverheadTiles);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+}  // extern "C"
+
+namespace {
+
+struct PrefixCache {
+    const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int len, cap;                     // cap: contiguous cache
+    const int32_t *table = nullptr;   // pages of a pool
+    int num_pages = 0;
+};
+
+int decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq, int nq, int q_cap,
+                  const PrefixCache &pre, const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+                  const uint8_t *v_scales, int Hkv, int kv_cap, const KvPages &pages, const int32_t *seqlens_k,
+                  int max_seqlen, int causal_in_block, float softmax_scale, int prefix_splits, int num_splits,
+                  void *workspace, size_t workspace_bytes, void *out, float *lse, int32_t *dev_status,
+                  cudaStream_t stream) {
+    int st;
+    if (!out || !aligned16(out)) return set_error(QK4V8_ERR_INVALID_ARG, "out must be a 16-byte aligned pointer");
+    if ((st = validate_packed(q_codes, q_scales, "Q"))) return st;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || nq < 1 || nq > 8 || (Hq / Hkv) * nq > 128 ||
+        static_cast<int64_t>(B) * (Hq / Hkv) * nq >= (int64_t{1} << 30))
+        return set_error(QK4V8_ERR_INVALID_ARG, "bad sizes B=%d Hq=%d Hkv=%d nq=%d", B, Hq, Hkv, nq);
+    if (q_cap <= 0 || q_cap % 128 || pre.len < 0 || max_seqlen < 0 || prefix_splits < 0 || num_splits < 0)
+        return set_error(QK4V8_ERR_INVALID_ARG, "bad lengths or splits: q_cap=%d prefix_len=%d max_seqlen=%d", q_cap,
+                         pre.len, max_seqlen);
+    if (pre.len > 0) {
+        if ((st = validate_packed(pre.k_codes, pre.k_scales, "prefix K")) ||
+            (st = validate_packed(pre.v_codes, pre.v_scales, "prefix V")))
+            return st;
+        if (!pre.table && (pre.cap <= 0 || pre.cap % 128 || pre.len > pre.cap))
+            return set_error(QK4V8_ERR_INVALID_ARG, "prefix_cap must be a multiple of 128 and >= prefix_len (%d, %d)",
+                             pre.cap, pre.len);
+    }
+    const int tiles = (pre.len + 127) / 128;
+    const int psplits = tiles == 0          ? 0
+                        : prefix_splits > 0 ? (prefix_splits < tiles ? prefix_splits : tiles)
+                                            : qk4v8_decode_prefix_default_splits(B, Hq, Hkv, nq, pre.len);
+    const int splits = max_seqlen == 0  ? 0
+                       : num_splits > 0 ? num_splits
+                                        : qk4v8_decode_default_splits(B, Hq, Hkv, nq, max_seqlen);
+    const size_t need = qk4v8_decode_prefix_workspace_bytes(B, Hq, nq, psplits, splits);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+        return set_error(QK4V8_ERR_INVALID_ARG, "workspace must be 16-byte aligned and >= %zu bytes", need);
+    const size_t own_bytes = qk4v8_decode_workspace_bytes(B, Hq, nq, splits);
+    const size_t rows = static_cast<size_t>(B) * Hq * nq;
+    float *po = static_cast<float *>(workspace);
+    float *pl = po + rows * psplits * 128;
+    float *own = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + (need - own_bytes));
+    if ((st = check_device())) return st;
+    qk4v8::PrefixParams p{};
+    CUtensorMap tk;
+    if (psplits > 0) {
+        const int64_t row_tiles = (static_cast<int64_t>(B) * (Hq / Hkv) * nq + 127) / 128;
+        if (row_tiles * Hkv * psplits >= (int64_t{1} << 31))
+            return set_error(QK4V8_ERR_INVALID_ARG, "too many rows and splits");
+        if ((st = make_k_map(&tk, pre.k_codes, pre.table ? pre.num_pages * Hkv : Hkv, pre.table ? 128 : pre.cap)))
+            return st;
+        p.q_codes = q_codes;
+        p.q_scales = q_scales;
+        p.k_scales = pre.k_scales;
+        p.v_codes = pre.v_codes;
+        p.v_scales = pre.v_scales;
+        p.table = pre.table;
+        p.num_pages = pre.num_pages;
+        p.row_blocks = pre.table ? 1 : pre.cap / 128;
+        p.Hq = Hq;
+        p.Hkv = Hkv;
+        p.G = Hq / Hkv;
+        p.nq = nq;
+        p.q_cap = q_cap;
+        p.len = pre.len;
+        p.tiles = tiles;
+        p.rows = B * p.G * nq;
+        p.row_tiles = static_cast<int>(row_tiles);
+        p.splits = psplits;
+        p.units = static_cast<int>(row_tiles * Hkv * psplits);
+        p.scale_log2 = resolve_scale(softmax_scale) * kLog2e;
+        p.ws_o = po;
+        p.ws_lse = pl;
+        p.status = dev_status;
+        p.test_stall = g_test_stall;
+    }
+    // The own keys first: its checks come before anything is enqueued.
+    if (splits > 0) {
+        int used = 0;
+        bool direct = false;
+        DecodeQuery q;
+        q.codes = q_codes;
+        q.scales = q_scales;
+        q.cap = q_cap;
+        if ((st = decode_splitkv(q, B, Hq, nq, k_codes, k_scales, v_codes, v_scales, Hkv, kv_cap, pages, seqlens_k,
+                                 max_seqlen, causal_in_block, 0, softmax_scale, splits, own, own_bytes, nullptr,
+                                 nullptr, dev_status, stream, &used, &direct)))
+            return st;
+    }
+    if (psplits > 0) {
+        const cudaError_t e = qk4v8::launch_prefix(tk, p, stream);
+        if (e != cudaSuccess) return cuda_error(e, "attention (prefix) launch");
+    }
+    const cudaError_t e = qk4v8::launch_prefix_merge(po, pl, psplits, own, own + rows * splits * 128, splits, B, Hq, nq,
+                                                     out, lse, stream);
+    return e == cudaSuccess ? QK4V8_OK : cuda_error(e, "prefix merge launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+int qk4v8_attention_decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq, int nq, int q_cap,
+                                  const uint8_t *p_k_codes, const uint8_t *p_k_scales, const uint8_t *p_v_codes,
+                                  const uint8_t *p_v_scales, int prefix_len, int prefix_cap, const uint8_t *k_codes,
+                                  const uint8_t *k_scales, const uint8_t *v_codes, const uint8_t *v_scales, int Hkv,
+                                  int kv_cap, const int32_t *seqlens_k, int max_seqlen, int causal_in_block,
+                                  float softmax_scale, int prefix_splits, int num_splits, void *workspace,
+                                  size_t workspace_bytes, void *out, float *lse, int32_t *dev_status, void *stream) {
+    const PrefixCache pre{p_k_codes, p_k_scales, p_v_codes, p_v_scales, prefix_len, prefix_cap};
+    return decode_prefix(q_codes, q_scales, B, Hq, nq, q_cap, pre, k_codes, k_scales, v_codes, v_scales, Hkv, kv_cap,
+                         KvPages{}, seqlens_k, max_seqlen, causal_in_block, softmax_scale, prefix_splits, num_splits,
+                         workspace, workspace_bytes, out, lse, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int qk4v8_attention_decode_prefix_paged(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq, int nq,
+                                        int q_cap, const uint8_t *k_codes, const uint8_t *k_scales,
+                                        const uint8_t *v_codes, const uint8_t *v_scales, int Hkv, int num_pages,
+                                        const int32_t *prefix_table, int prefix_len, const int32_t *block_table,
+                                        int max_pages, const int32_t *seqlens_k, int max_seqlen, int causal_in_block,
+                                        float softmax_scale, int prefix_splits, int num_splits, void *workspace,
+                                        size_t workspace_bytes, void *out, float *lse, int32_t *dev_status,
+                                        void *stream) {
+    if (!block_table || !prefix_table) return set_error(QK4V8_ERR_INVALID_ARG, "block_table or prefix_table is null");
+    if (max_pages <= 0 || max_pages >= (1 << 24) || num_pages <= 0 || Hkv <= 0 ||
+        static_cast<int64_t>(num_pages) * Hkv >= (int64_t{1} << 31))
+        return set_error(QK4V8_ERR_INVALID_ARG, "bad page pool: num_pages=%d max_pages=%d", num_pages, max_pages);
+    PrefixCache pre{k_codes, k_scales, v_codes, v_scales, prefix_len, 0};
+    pre.table = prefix_table;
+    pre.num_pages = num_pages;
+    KvPages pages;
+    pages.block_table = block_table;
+    pages.max_pages = max_pages;
+    pages.num_pages = num_pages;
+    return decode_prefix(q_codes, q_scales, B, Hq, nq, q_cap, pre, k_codes, k_scales, v_codes, v_scales, Hkv,
+                         max_pages * 128, pages, seqlens_k, max_seqlen, causal_in_block, softmax_scale, prefix_splits,
+                         num_splits, workspace, workspace_bytes, out, lse, dev_status,
+                         static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -31,6 +31,7 @@
 #include "mx_encode.cuh"
 #include "ptx.cuh"
 #include "qk4v8_internal.h"
+#include "rope.cuh"
 
 namespace qk4v8 {
 
@@ -214,6 +215,296 @@ cudaError_t launch_kv_append(const void *k, const void *v, int B, int n_new, int
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !in_place) return e;
     kv_advance_lengths_kernel<<<(B + 255) / 256, 256, 0, stream>>>(seqlens_out, B, n_new);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------ append with the position rotation
+
+// The append of a model with rotary positions: K rows are rotated (rope.cuh) on
+// their way into MXFP4, V is packed as above, and every sequence may bring its own
+// number of new tokens (a padded batch).
+//
+// One launch, two kinds of CTA of 256 threads:
+//  - K: a warp takes a few tokens by up to 32 heads, eight lanes per row, so that a
+//    token's cosines and sines are read once for its heads;
+//  - V: CTA (b, h, page) takes the 32-token groups of one page that the new tokens
+//    touch. It stages their bf16 rows in shared memory (16-byte loads along the
+//    channels; rows from before the append come from the staging buffer), and
+//    thread (channel pair, group) encodes 32 tokens of two channels from there. The
+//    codes go out through shared memory as whole 32-byte sectors, so a full page is
+//    16 KiB contiguous. (The append above loads two bytes per thread and token.)
+//    The CTA of the first page is the only reader of the staging rows, so it also
+//    refreshes them, after its own reads.
+//
+// Bound by memory: 512 bytes read and 200 written per new token and head; a single
+// token of a sequence rewrites its open group, 4 KB per head.
+struct KvAppendRopeArgs {
+    const __nv_bfloat16 *k, *v;
+    int B, n, H;
+    int64_t ksb, kst, ksh, vsb, vst, vsh;
+    const int32_t *seqlens, *new_lens;
+    int32_t *seqlens_out;  // null, or another array than seqlens
+    const int32_t *block_table;
+    int max_pages, num_pages;
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    __nv_bfloat16 *tail;
+    int32_t *status;
+    RopeParams rope;
+    RopeTiling tile;
+    int64_t k_ctas;
+    int v_pages;  // pages that n tokens can touch
+};
+
+// New tokens of sequence b: new_lens[b] (none: all n), held to 0..n.
+__device__ __forceinline__ int append_count(const KvAppendRopeArgs &a, int b) {
+    if (!a.new_lens) return a.n;
+    const int m = a.new_lens[b];
+    if (m >= 0 && m <= a.n) return m;
+    flag_bad_page(a.status);
+    return m < 0 ? 0 : a.n;
+}
+
+template <bool kAdjacent, bool kHadamard>
+__device__ __forceinline__ void append_k_rows(const KvAppendRopeArgs &a) {
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int per_b = a.tile.token_groups * a.tile.head_chunks;
+    const int b = static_cast<int>(item / per_b);
+    if (b >= a.B) return;
+    const int rem = static_cast<int>(item - static_cast<int64_t>(b) * per_b);
+    const int tg = rem / a.tile.head_chunks, hc = rem - tg * a.tile.head_chunks;
+    const int lane = threadIdx.x & 31, j = lane & 7, slot = lane >> 3;
+    const int hs = 1 << a.tile.hs_log2;
+    const int t = tg * (4 >> a.tile.hs_log2) + (slot >> a.tile.hs_log2);
+    const int h_end = min(a.H, (hc + 1) * a.tile.heads);
+    const int L0 = a.seqlens[b];
+    int page = -1;
+    const bool mine = t < append_count(a, b);
+    // (L0 + t cannot pass 2^31 within the pages: L0 < max_pages * 128 < 2^31 - n.)
+    if (mine) {
+        page = L0 <= a.max_pages * 128 ? page_of(a.block_table, a.max_pages, a.num_pages, b, L0 < 0 ? -1 : L0 + t) : -1;
+        if (page < 0 && j == 0) flag_bad_page(a.status);
+    }
+    const bool live = page >= 0;
+    const int nrot = a.rope.rotary >> 4;
+    RopeTrig g;
+    rope_load<kAdjacent>(a.rope, b, t, L0, j, live, a.status, g);
+    int k0, k1;
+    rope_chunks(kAdjacent, nrot, j, k0, k1);
+    const __nv_bfloat16 *xt = a.k + b * a.ksb + static_cast<int64_t>(t) * a.kst;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    int h = hc * a.tile.heads + (slot & (hs - 1));
+    uint4 r0 = zero, r1 = zero;
+    if (live && h < h_end) {
+        r0 = *reinterpret_cast<const uint4 *>(xt + h * a.ksh + k0 * 8);
+        r1 = *reinterpret_cast<const uint4 *>(xt + h * a.ksh + k1 * 8);
+    }
+    const int rr = (L0 + t) & 127;
+    for (int h0 = hc * a.tile.heads; h0 < h_end; h0 += hs, h += hs) {
+        uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+        r0 = r1 = zero;
+        if (live && h + hs < h_end) {
+            r0 = *reinterpret_cast<const uint4 *>(xt + (h + hs) * a.ksh + k0 * 8);
+            r1 = *reinterpret_cast<const uint4 *>(xt + (h + hs) * a.ksh + k1 * 8);
+        }
+        rope_row<kAdjacent>(g, nrot, j, w0, w1);
+        uint32_t c0, c1, sf;
+        mxfp4_row8<kHadamard>(w0, w1, j, c0, c1, sf);
+        if (live && h < h_end) {
+            const int64_t row = static_cast<int64_t>(page) * a.H + h;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(a.k_codes + (row * 128 + rr) * 64);
+            dst[j] = c0;
+            dst[j + 8] = c1;
+            if (j == 0)
+                *reinterpret_cast<uint32_t *>(a.k_scales + row * 512 + (rr & 31) * 16 + (rr >> 5) * 4) = sf;
+        }
+    }
+}
+
+__device__ __forceinline__ void append_v_page(const KvAppendRopeArgs &a, int64_t idx) {
+    constexpr int kPitch = 136;   // bf16 elements per staged token row (16 bytes of padding)
+    constexpr int kCPitch = 144;  // bytes per staged code row
+    __shared__ __align__(16) uint16_t tile[128 * kPitch];
+    __shared__ __align__(4) uint8_t atom[512];
+    uint8_t *ctile = reinterpret_cast<uint8_t *>(tile);
+    const int64_t bh = idx / a.v_pages;
+    const int pg = static_cast<int>(idx - bh * a.v_pages);
+    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+    const int L0 = a.seqlens[b];
+    const int m = append_count(a, b);
+    if (pg == 0 && h == 0 && threadIdx.x == 0 && a.seqlens_out) a.seqlens_out[b] = L0 + m;
+    if (m == 0) return;
+    if (L0 < 0 || L0 > a.max_pages * 128) {
+        if (threadIdx.x == 0) flag_bad_page(a.status);
+        return;
+    }
+    const int L1 = L0 + m;
+    const int p0 = ((L0 >> 7) + pg) * 128;  // first token of the page
+    if (p0 >= L1) return;
+    const int lo = max(L0 & ~31, p0), hi = min((L1 + 31) & ~31, p0 + 128);  // touched groups' tokens
+    const int page = page_of(a.block_table, a.max_pages, a.num_pages, b, p0);
+    if (page < 0 && threadIdx.x == 0) flag_bad_page(a.status);
+    uint16_t *tail = reinterpret_cast<uint16_t *>(a.tail) + bh * (32 * 128);
+    const uint16_t *vin = reinterpret_cast<const uint16_t *>(a.v) + b * a.vsb + h * a.vsh;
+    uint4 raw[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // every load of the thread before its first store
+        const int i = threadIdx.x + 256 * k;
+        const int t = p0 + (i >> 4), ch = (i & 15) * 8;
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (t >= lo && t < hi) {
+            if (t < L0)
+                raw[k] = *reinterpret_cast<const uint4 *>(tail + (t & 31) * 128 + ch);
+            else if (t < L1)
+                raw[k] = *reinterpret_cast<const uint4 *>(vin + static_cast<int64_t>(t - L0) * a.vst + ch);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int i = threadIdx.x + 256 * k;
+        const int tk = i >> 4;
+        if (p0 + tk >= lo && p0 + tk < hi)
+            *reinterpret_cast<uint4 *>(&tile[tk * kPitch + (i & 15) * 8]) = raw[k];
+    }
+    __syncthreads();
+    if (pg == 0 && (L1 & 31) != 0) {
+        // The open group after the append, in slots t % 32. (Its rows from before the
+        // append are in place; the old rows were read above.)
+        const int t0 = max(L1 & ~31, L0);
+        for (int i = threadIdx.x; i < (L1 - t0) * 16; i += 256) {
+            const int t = t0 + (i >> 4), ch = (i & 15) * 8;
+            *reinterpret_cast<uint4 *>(tail + (t & 31) * 128 + ch) =
+                *reinterpret_cast<const uint4 *>(vin + static_cast<int64_t>(t - L0) * a.vst + ch);
+        }
+    }
+    if (page < 0) return;
+    const int cp = threadIdx.x & 63, grp = threadIdx.x >> 6;
+    const bool on = p0 + grp * 32 >= lo && p0 + grp * 32 < hi;
+    uint32_t words[2][8];
+    int X[2] = {-127, -127};
+    if (on) {
+        const uint32_t *t32 = reinterpret_cast<const uint32_t *>(tile);
+        uint32_t w[32];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            w[i] = t32[(grp * 32 + i) * (kPitch / 2) + cp];
+            mx = __vmaxu2(mx, w[i] & 0x7FFF7FFFu);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            X[q] = shared_exponent(q ? bf16_hi(mx) : bf16_lo(mx), 8);
+            const float f = pow2_neg(X[q]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // x / 2^X is exact; the conversion keeps the sign, also of a value that
+                // rounds to zero.
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = (q ? bf16_hi(w[4 * i + e]) : bf16_lo(w[4 * i + e])) * f;
+                words[q][i] = cvt_e4m3x2(y[0], y[1]) | (static_cast<uint32_t>(cvt_e4m3x2(y[2], y[3])) << 16);
+            }
+        }
+    }
+    __syncthreads();  // the staged rows have been read
+    if (on) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int c = 2 * cp + q;
+            // Staged code rows: channel 2cp at row cp, 2cp + 1 at row 64 + cp, so that a
+            // warp stores to consecutive rows.
+            uint4 *dst = reinterpret_cast<uint4 *>(&ctile[(cp + 64 * q) * kCPitch + grp * 32]);
+            dst[0] = make_uint4(words[q][0], words[q][1], words[q][2], words[q][3]);
+            dst[1] = make_uint4(words[q][4], words[q][5], words[q][6], words[q][7]);
+            atom[(c & 31) * 16 + (c >> 5) * 4 + grp] = static_cast<uint8_t>(X[q] + 127);
+        }
+    }
+    __syncthreads();
+    const int64_t row = static_cast<int64_t>(page) * a.H + h;
+    uint8_t *block = a.v_codes + row * (128 * 128);
+    const int g0 = (lo - p0) >> 5, ng = (hi - lo) >> 5;  // touched groups: [g0, g0 + ng)
+    for (int i = threadIdx.x; i < 128 * 8; i += 256) {
+        const int c = i >> 3, ch = i & 7;
+        if ((ch >> 1) >= g0 && (ch >> 1) < g0 + ng)
+            *reinterpret_cast<uint4 *>(block + c * 128 + ch * 16) =
+                *reinterpret_cast<const uint4 *>(&ctile[((c >> 1) + (c & 1) * 64) * kCPitch + ch * 16]);
+    }
+    if (threadIdx.x < 128) {  // the channel's four scale bytes, those of the touched groups
+        const int at = (threadIdx.x & 31) * 16 + (threadIdx.x >> 5) * 4;
+        uint8_t *dst = a.v_scales + row * 512 + at;
+        if (ng == 4)
+            *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(atom + at);
+        else
+            for (int g = g0; g < g0 + ng; ++g) dst[g] = atom[at + g];
+    }
+}
+
+template <bool kAdjacent, bool kHadamard>
+__global__ void __launch_bounds__(256, 3) kv_append_rope_kernel(const __grid_constant__ KvAppendRopeArgs a) {
+    if (blockIdx.x < a.k_ctas)
+        append_k_rows<kAdjacent, kHadamard>(a);
+    else
+        append_v_page(a, static_cast<int64_t>(blockIdx.x) - a.k_ctas);
+}
+
+// seqlens[b] += new_lens[b] (held to 0..n) in place, after every reader of seqlens ran.
+__global__ void kv_advance_ragged_kernel(int32_t *seqlens, const int32_t *new_lens, int B, int n) {
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b < B) seqlens[b] += new_lens ? min(max(new_lens[b], 0), n) : n;
+}
+
+cudaError_t launch_kv_append_rope(const void *k, const void *v, int B, int n, int H, const int64_t (&ks)[3],
+                                  const int64_t (&vs)[3], const int32_t *seqlens, const int32_t *new_lens,
+                                  int32_t *seqlens_out, const int32_t *block_table, int max_pages, int num_pages,
+                                  uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales,
+                                  void *tail, const RopeParams &rope, bool hadamard_k, int32_t *status,
+                                  cudaStream_t stream) {
+    const bool in_place = seqlens_out == seqlens;
+    KvAppendRopeArgs a{};
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.B = B;
+    a.n = n;
+    a.H = H;
+    a.ksb = ks[0];
+    a.kst = ks[1];
+    a.ksh = ks[2];
+    a.vsb = vs[0];
+    a.vst = vs[1];
+    a.vsh = vs[2];
+    a.seqlens = seqlens;
+    a.new_lens = new_lens;
+    a.seqlens_out = in_place ? nullptr : seqlens_out;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.k_codes = k_codes;
+    a.k_scales = k_scales;
+    a.v_codes = v_codes;
+    a.v_scales = v_scales;
+    a.tail = static_cast<__nv_bfloat16 *>(tail);
+    a.status = status;
+    a.rope = rope;
+    a.tile = rope_tiling(B, n, H);
+    const int64_t per_b = static_cast<int64_t>(a.tile.token_groups) * a.tile.head_chunks;
+    a.k_ctas = (B * per_b + 7) / 8;
+    a.v_pages = (n + 126) / 128 + 1;
+    const int64_t grid = a.k_ctas + static_cast<int64_t>(B) * H * a.v_pages;
+    if (per_b >= (int64_t{1} << 31) || grid >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+    const unsigned g = static_cast<unsigned>(grid);
+    if (rope.adjacent) {
+        if (hadamard_k)
+            kv_append_rope_kernel<true, true><<<g, 256, 0, stream>>>(a);
+        else
+            kv_append_rope_kernel<true, false><<<g, 256, 0, stream>>>(a);
+    } else {
+        if (hadamard_k)
+            kv_append_rope_kernel<false, true><<<g, 256, 0, stream>>>(a);
+        else
+            kv_append_rope_kernel<false, false><<<g, 256, 0, stream>>>(a);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !in_place) return e;
+    kv_advance_ragged_kernel<<<(B + 255) / 256, 256, 0, stream>>>(seqlens_out, new_lens, B, n);
     return cudaGetLastError();
 }
 

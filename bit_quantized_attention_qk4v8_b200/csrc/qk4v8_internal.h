@@ -104,6 +104,48 @@ cudaError_t launch_kv_append(const void *k, const void *v, int B, int n_new, int
                              int num_pages, uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes,
                              uint8_t *v_scales, void *tail, bool rotate_k, int32_t *seqlens_out, int32_t *status,
                              cudaStream_t stream);
+// The prefix part of a shared-prefix decode (prefix.cu).
+struct PrefixParams {
+    const uint8_t *q_codes, *q_scales;            // [B][Hq][q_cap]
+    const uint8_t *k_scales, *v_codes, *v_scales; // [rows][row_blocks] blocks of 128 tokens
+    const int32_t *table;                         // pages of the prefix's tiles; null: contiguous
+    int num_pages, row_blocks;
+    int Hq, Hkv, G, nq, q_cap;
+    int len, tiles;                               // tokens of the prefix, and 128-key tiles
+    int rows, row_tiles;                          // query rows of a KV head (B * G * nq), and 128-row tiles
+    int splits, units;                            // units = splits * Hkv * row_tiles
+    float scale_log2;
+    float *ws_o, *ws_lse;                         // [B][Hq][nq][splits][128], [B][Hq][nq][splits]
+    int32_t *status;
+    int test_stall;
+};
+cudaError_t launch_prefix(const CUtensorMap &tmap_k, const PrefixParams &p, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const float *o, const float *l, int splits, const float *own_o, const float *own_l,
+                                int own_splits, int B, int Hq, int nq, void *out, float *lse, cudaStream_t stream);
+// Rotary positions of a call, as the kernels take them (rope.cuh).
+struct RopeParams {
+    const float *table;         // (cos, sin) [max_pos][rotary / 2][2]
+    int max_pos, rotary;        // rotary: a multiple of 16, up to 128
+    int adjacent;               // pairs (2i, 2i + 1) instead of (i, i + rotary / 2)
+    int n_axes;                 // 1..4
+    uint64_t pair_axis[2];      // two bits per pair
+    const int32_t *positions;   // null: the same token index on every axis
+    int64_t pos_sa, pos_sb, pos_st;
+};
+// MXFP4 of the rotated rows (after the Hadamard rotation with `rotate`). pad: write
+// all `cap` token rows, else the S given ones.
+cudaError_t launch_quantize_qk_rope(const void *x, int B, int S, int H, int64_t sb, int64_t ss, int64_t sh,
+                                    const int32_t *seqlens, const int32_t *start, int cap, const RopeParams &rope,
+                                    bool rotate, bool pad, uint8_t *codes, uint8_t *scales, int32_t *status,
+                                    cudaStream_t stream);
+// Paged append with K rotated, new_lens[b] (null: n) tokens of each sequence; ks, vs:
+// strides of batch, token and head.
+cudaError_t launch_kv_append_rope(const void *k, const void *v, int B, int n, int H, const int64_t (&ks)[3],
+                                  const int64_t (&vs)[3], const int32_t *seqlens, const int32_t *new_lens,
+                                  int32_t *seqlens_out, const int32_t *block_table, int max_pages, int num_pages,
+                                  uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales,
+                                  void *tail, const RopeParams &rope, bool hadamard_k, int32_t *status,
+                                  cudaStream_t stream);
 cudaError_t launch_decode_merge(const float *ws_o, const float *ws_lse, int B, int Hq, int nq, int splits,
                                 __nv_bfloat16 *out, float *lse, cudaStream_t stream);
 

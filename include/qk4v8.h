@@ -416,6 +416,129 @@ QK4V8_API int qk4v8_attention_decode_bf16_paged(const void *q, int B, int Hq, in
                                                 void *stream);
 
 /*
+ * Rotary positions, of one or several axes, as the two calls below take them.
+ *   table      float [max_pos][rotary_dim / 2][2] (device, 16-byte aligned): the
+ *              cosine and the sine of position p times pair i's frequency, with any
+ *              scaling of the model in them
+ *   rotary_dim channels that turn, a multiple of 16 up to 128: the first rotary_dim
+ *              of a row; the others pass through
+ *   adjacent   0: pair i is channels (i, i + rotary_dim / 2); 1: (2i, 2i + 1)
+ *   n_axes     1..4 position axes (one for text; time, height and width for images
+ *              and video)
+ *   pair_axis  uint8 [rotary_dim / 2] (HOST, nullable: axis 0 for all): the axis
+ *              whose position turns pair i, so any split or interleaving of the axes
+ *   positions  int32 (device, nullable): position of token t of sequence b on axis a
+ *              at positions[a * pos_stride_axis + b * pos_stride_b + t * pos_stride_t]
+ *              (a stride of 0 shares it). Null: every axis has the token's index,
+ *              see the calls.
+ * A pair (x_a, x_b) becomes (x_a c - x_b s, x_b c + x_a s); each value is rounded to
+ * nearest even, from fp64 by way of fp32 to bf16, so the result does not depend on
+ * the order of operations and equals a rotation in bf16 activations followed by
+ * the plain quantizer. Inputs are finite. A position outside [0, max_pos) reads
+ * table row 0 and writes QK4V8_ERR_INVALID_ARG to *dev_status.
+ */
+typedef struct {
+    const float *table;
+    int max_pos, rotary_dim, adjacent, n_axes;
+    const uint8_t *pair_axis;
+    const int32_t *positions;
+    int64_t pos_stride_axis, pos_stride_b, pos_stride_t;
+} qk4v8_rope;
+
+/*
+ * MXFP4 quantization of Q or K after its position rotation, in one pass: the same
+ * bytes as rotating into bf16 and then qk4v8_quantize_qk (or, with hadamard,
+ * qk4v8_quantize_qk_hadamard).
+ *   rope     as above; without positions, token t of sequence b is at start[b] + t
+ *   start    int32 [B] (device, nullable: 0)
+ *   pad      1: every token row < cap is written, rows past S or seqlens[b] as
+ *            padding; 0: only the S given rows are (rows past seqlens[b] as padding),
+ *            the rest of the buffers is left as it is: for decode and verify calls,
+ *            which read no other row, without the writes of a whole capacity
+ *   other arguments, layout and errors as for qk4v8_quantize_qk.
+ */
+QK4V8_API int qk4v8_quantize_qk_rope(const void *x, int B, int S, int H, int d, int64_t stride_b, int64_t stride_s,
+                                     int64_t stride_h, const int32_t *seqlens, const int32_t *start,
+                                     const qk4v8_rope *rope, int hadamard, int cap, int pad, uint8_t *codes,
+                                     uint8_t *scales, int32_t *dev_status, void *stream);
+
+/*
+ * qk4v8_kv_append with K rotated on its way into the pages, and with a number of new
+ * tokens per sequence.
+ *   k_new, v_new  bf16 [B][n_new][Hkv][128], strides {batch, token, head} each
+ *   rope      as above; without positions, a token is at its place in the sequence,
+ *             seqlens[b] + t
+ *   new_lens  int32 [B] (device, nullable: n_new for all): the sequence's first
+ *             new_lens[b] tokens are appended, 0 touches nothing of it. A count
+ *             outside 0..n_new is held to that range and reported in *dev_status.
+ *   seqlens_out  (device, nullable, may be seqlens) receives seqlens[b] + new_lens[b]
+ *   pages, v_tail, hadamard_k, dev_status and errors as for qk4v8_kv_append: the pages
+ *   hold what qk4v8_quantize_qk_rope and qk4v8_quantize_v of the whole sequence give,
+ *   after any run of appends by either call. A token without a valid page is skipped
+ *   and reported. seqlens[b] below 0 or past max_pages * 128 skips the sequence.
+ */
+QK4V8_API int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, int n_new, int Hkv, int d,
+                                   const int64_t *k_strides, const int64_t *v_strides, const int32_t *seqlens,
+                                   const int32_t *new_lens, int32_t *seqlens_out, const qk4v8_rope *rope,
+                                   const int32_t *block_table, int max_pages, int num_pages, uint8_t *k_codes,
+                                   uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales, void *v_tail,
+                                   int hadamard_k, int32_t *dev_status, void *stream);
+
+/*
+ * Decode over a shared prefix: B sequences whose caches begin with the same
+ * prefix_len tokens, held once. Every query row sees all keys of the prefix, and
+ * of its own sequence's keys what it would see in qk4v8_attention_decode (with
+ * causal_in_block, query t of nq the keys j <= seqlens_k[b] - nq + t). The
+ * result is attention over both: the prefix is read once for 128 query rows
+ * (128 / (G * nq) sequences) rather than once for each sequence.
+ *   q_*      packed MXFP4 Q, [B][Hq][q_cap], nq (1..8) tokens (the rows past nq
+ *            are not read by the prefix part)
+ *   p_k_*, p_v_*  packed MXFP4 K and MXFP8 V of the prefix, [1][Hkv][prefix_cap]
+ *            (the quantize calls with B = 1); prefix_len >= 0
+ *   k_*, v_* the sequences' own caches, seqlens_k int32 [B] their lengths, which may
+ *            be 0; max_seqlen a host bound on them, 0 when all are empty
+ *   prefix_splits  parts the prefix is cut into, at most its 128-key tiles (0:
+ *            qk4v8_decode_prefix_default_splits); num_splits as for
+ *            qk4v8_attention_decode
+ *   workspace  qk4v8_decode_prefix_workspace_bytes(B, Hq, nq, prefix_splits,
+ *            num_splits) bytes with the counts used, 16-byte aligned. Calls that may
+ *            overlap on the GPU need one each.
+ *   out, lse, softmax_scale, dev_status and errors as for qk4v8_attention_decode. A
+ *            row with no key at all outputs 0 with lse = -inf.
+ * Needs (Hq / Hkv) * nq <= 128. Three launches: the prefix kernel, the split kernel
+ * of qk4v8_attention_decode over the own keys, the merge.
+ *
+ * qk4v8_attention_decode_prefix_paged: the same over a pool of pages (see
+ * qk4v8_kv_append): prefix_table int32 [ceil(prefix_len / 128)] (device) lists the
+ * prefix's pages, block_table and seqlens_k hold the own parts, which begin on a
+ * page of their own. Up to 64 query rows per KV head. A page index outside the pool
+ * reads page 0 and reports QK4V8_ERR_INVALID_ARG in *dev_status.
+ */
+QK4V8_API size_t qk4v8_decode_prefix_workspace_bytes(int B, int Hq, int nq, int prefix_splits, int num_splits);
+
+QK4V8_API int qk4v8_decode_prefix_default_splits(int B, int Hq, int Hkv, int nq, int prefix_len);
+
+QK4V8_API int qk4v8_attention_decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq, int nq,
+                                            int q_cap, const uint8_t *p_k_codes, const uint8_t *p_k_scales,
+                                            const uint8_t *p_v_codes, const uint8_t *p_v_scales, int prefix_len,
+                                            int prefix_cap, const uint8_t *k_codes, const uint8_t *k_scales,
+                                            const uint8_t *v_codes, const uint8_t *v_scales, int Hkv, int kv_cap,
+                                            const int32_t *seqlens_k, int max_seqlen, int causal_in_block,
+                                            float softmax_scale, int prefix_splits, int num_splits, void *workspace,
+                                            size_t workspace_bytes, void *out, float *lse, int32_t *dev_status,
+                                            void *stream);
+
+QK4V8_API int qk4v8_attention_decode_prefix_paged(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq,
+                                                  int nq, int q_cap, const uint8_t *k_codes, const uint8_t *k_scales,
+                                                  const uint8_t *v_codes, const uint8_t *v_scales, int Hkv,
+                                                  int num_pages, const int32_t *prefix_table, int prefix_len,
+                                                  const int32_t *block_table, int max_pages, const int32_t *seqlens_k,
+                                                  int max_seqlen, int causal_in_block, float softmax_scale,
+                                                  int prefix_splits, int num_splits, void *workspace,
+                                                  size_t workspace_bytes, void *out, float *lse, int32_t *dev_status,
+                                                  void *stream);
+
+/*
  * Decode step from bf16 queries (MpFA QK4V8 article, section 3.2: the query's
  * MXFP4 scales are computed as it is loaded, inside the attention call).
  * Same result, bit for bit, as qk4v8_quantize_qk (capacity 128) followed by
