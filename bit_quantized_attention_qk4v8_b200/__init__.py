@@ -30,8 +30,7 @@ __all__ = [
     "attention_decode_bf16", "decode_bf16_workspace_bytes",
     "paged_kv", "kv_append", "attention_decode_paged", "attention_decode_bf16_paged", "quantize_v4",
     "Rope", "rope_table", "quantize_qk_rope", "kv_append_rope",
-    "attention_decode_prefix", "attention_decode_prefix_paged", "decode_prefix_default_splits",
-    "decode_prefix_workspace_bytes",
+    "attention_decode_prefix", "attention_decode_prefix_paged", "decode_prefix_workspace_bytes",
 ]
 
 D = 128
@@ -638,43 +637,26 @@ def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rop
 # ----------------------------------------------------------------------------------------------------------
 # Decode over a shared prefix (include/qk4v8.h: qk4v8_attention_decode_prefix).
 
-def decode_prefix_workspace_bytes(B: int, Hq: int, nq: int, prefix_splits: int, num_splits: int) -> int:
-    return int(lib().qk4v8_decode_prefix_workspace_bytes(B, Hq, nq, prefix_splits, num_splits))
+def decode_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, nq: int, prefix_len: int, max_seqlen: int) -> int:
+    return int(lib().qk4v8_decode_prefix_workspace_bytes(B, Hq, Hkv, nq, prefix_len, max_seqlen))
 
 
-def decode_prefix_default_splits(B: int, Hq: int, Hkv: int, nq: int, prefix_len: int) -> int:
-    return int(lib().qk4v8_decode_prefix_default_splits(B, Hq, Hkv, nq, prefix_len))
-
-
-def _prefix_buffers(q: MXFP4, Hkv: int, prefix_len: int, max_seqlen: int, prefix_splits: int, num_splits: int,
-                    workspace, out, lse, return_lse):
+def _prefix_buffers(q: MXFP4, Hkv: int, prefix_len: int, max_seqlen: int, workspace, out, lse, return_lse):
     dev = q.codes.device
-    B, Hq, nq = q.B, q.H, q.length
-    tiles = (prefix_len + 127) // 128
-    if tiles == 0:
-        ps = 0
-    elif prefix_splits > 0:
-        ps = min(prefix_splits, tiles)
-    else:
-        ps = decode_prefix_default_splits(B, Hq, Hkv, nq, prefix_len)
-    if max_seqlen == 0:
-        ns = 0
-    else:
-        ns = num_splits if num_splits > 0 else decode_default_splits(B, Hq, Hkv, nq, max_seqlen)
     if workspace is None:
-        workspace = torch.empty((max(16, decode_prefix_workspace_bytes(B, Hq, nq, ps, ns)),), dtype=torch.uint8,
-                                device=dev)
+        need = decode_prefix_workspace_bytes(q.B, q.H, Hkv, q.length, prefix_len, max_seqlen)
+        workspace = torch.empty((max(16, need),), dtype=torch.uint8, device=dev)
     if out is None:
-        out = torch.empty((B, nq, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((q.B, q.length, q.H, D), dtype=torch.bfloat16, device=dev)
     if return_lse and lse is None:
-        lse = torch.empty((B, Hq, nq), dtype=torch.float32, device=dev)
-    return ps, ns, workspace, workspace.numel() * workspace.element_size(), out, lse
+        lse = torch.empty((q.B, q.H, q.length), dtype=torch.float32, device=dev)
+    return workspace, workspace.numel() * workspace.element_size(), out, lse
 
 
 def attention_decode_prefix(q: MXFP4, k_prefix: MXFP4, v_prefix: MXFP8V, k: MXFP4, v: MXFP8V, seqlens_k,
                             max_seqlen: Optional[int] = None, prefix_len: Optional[int] = None,
                             causal_in_block: bool = True, softmax_scale: Optional[float] = None,
-                            prefix_splits: int = 0, num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None,
                             out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                             return_lse: bool = False, dev_status: Optional[torch.Tensor] = None):
     """Decode / verify of sequences that share a prefix (k_prefix, v_prefix: packed with B = 1), followed by their
@@ -693,21 +675,20 @@ def attention_decode_prefix(q: MXFP4, k_prefix: MXFP4, v_prefix: MXFP8V, k: MXFP
     prefix_len = k_prefix.length if prefix_len is None else int(prefix_len)
     max_seqlen = k.cap if max_seqlen is None else int(max_seqlen)
     sl = _seqlens(seqlens_k, B, dev)
-    ps, ns, ws, ws_bytes, out, lse = _prefix_buffers(q, k.H, prefix_len, max_seqlen, prefix_splits, num_splits,
-                                                     workspace, out, lse, return_lse)
+    ws, ws_bytes, out, lse = _prefix_buffers(q, k.H, prefix_len, max_seqlen, workspace, out, lse, return_lse)
     with torch.cuda.device(dev):
         check(lib().qk4v8_attention_decode_prefix(
             q.codes.data_ptr(), q.scales.data_ptr(), B, Hq, nq, q.cap, k_prefix.codes.data_ptr(),
             k_prefix.scales.data_ptr(), v_prefix.codes.data_ptr(), v_prefix.scales.data_ptr(), prefix_len, k_prefix.cap,
             k.codes.data_ptr(), k.scales.data_ptr(), v.codes.data_ptr(), v.scales.data_ptr(), k.H, k.cap, _ptr(sl),
-            max_seqlen, int(bool(causal_in_block)), float(softmax_scale or 0.0), ps, ns, ws.data_ptr(), ws_bytes,
-            out.data_ptr(), _ptr(lse), _ptr(dev_status), _stream(dev)), "qk4v8_attention_decode_prefix")
+            max_seqlen, int(bool(causal_in_block)), float(softmax_scale or 0.0), ws.data_ptr(), ws_bytes, out.data_ptr(),
+            _ptr(lse), _ptr(dev_status), _stream(dev)), "qk4v8_attention_decode_prefix")
     return (out, lse) if return_lse else out
 
 
 def attention_decode_prefix_paged(q: MXFP4, cache: PagedKV, prefix_table: torch.Tensor, prefix_len: int,
                                   max_seqlen: int, causal_in_block: bool = True,
-                                  softmax_scale: Optional[float] = None, prefix_splits: int = 0, num_splits: int = 0,
+                                  softmax_scale: Optional[float] = None,
                                   workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                                   lse: Optional[torch.Tensor] = None, return_lse: bool = False,
                                   dev_status: Optional[torch.Tensor] = None):
@@ -723,14 +704,13 @@ def attention_decode_prefix_paged(q: MXFP4, cache: PagedKV, prefix_table: torch.
     if prefix_table.dtype != torch.int32 or prefix_table.device != dev or prefix_table.dim() != 1 or \
             not prefix_table.is_contiguous() or prefix_table.shape[0] * 128 < prefix_len:
         raise ValueError("prefix_table must be a contiguous int32 tensor of the prefix's pages on q's device")
-    ps, ns, ws, ws_bytes, out, lse = _prefix_buffers(q, cache.Hkv, prefix_len, max_seqlen, prefix_splits, num_splits,
-                                                     workspace, out, lse, return_lse)
+    ws, ws_bytes, out, lse = _prefix_buffers(q, cache.Hkv, prefix_len, max_seqlen, workspace, out, lse, return_lse)
     with torch.cuda.device(dev):
         check(lib().qk4v8_attention_decode_prefix_paged(
             q.codes.data_ptr(), q.scales.data_ptr(), B, Hq, nq, q.cap, cache.k_codes.data_ptr(),
             cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), cache.Hkv, cache.num_pages,
             prefix_table.data_ptr(), prefix_len, cache.block_table.data_ptr(), cache.max_pages,
-            cache.seqlens.data_ptr(), max_seqlen, int(bool(causal_in_block)), float(softmax_scale or 0.0), ps, ns,
+            cache.seqlens.data_ptr(), max_seqlen, int(bool(causal_in_block)), float(softmax_scale or 0.0),
             ws.data_ptr(), ws_bytes, out.data_ptr(), _ptr(lse), _ptr(dev_status), _stream(dev)),
             "qk4v8_attention_decode_prefix_paged")
     return (out, lse) if return_lse else out

@@ -71,14 +71,13 @@ SIGNATURES = {
                                 _vp, _vp, _vp], _i32),
     "qk4v8_kv_append_rope": ([_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp,
                               _vp, _vp, _vp, _vp, _i32, _vp, _vp], _i32),
-    "qk4v8_decode_prefix_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32], _sz),
-    "qk4v8_decode_prefix_default_splits": ([_i32, _i32, _i32, _i32, _i32], _i32),
+    "qk4v8_decode_prefix_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32], _sz),
     "qk4v8_attention_decode_prefix": ([_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp,
-                                       _vp, _vp, _i32, _i32, _vp, _i32, _i32, _f32, _i32, _i32, _vp, _sz, _vp, _vp,
-                                       _vp, _vp], _i32),
+                                       _vp, _vp, _i32, _i32, _vp, _i32, _i32, _f32, _vp, _sz, _vp, _vp, _vp, _vp],
+                                      _i32),
     "qk4v8_attention_decode_prefix_paged": ([_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp,
-                                             _i32, _vp, _i32, _vp, _i32, _i32, _f32, _i32, _i32, _vp, _sz, _vp, _vp,
-                                             _vp, _vp], _i32),
+                                             _i32, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _sz, _vp, _vp, _vp, _vp],
+                                            _i32),
     "qk4v8_decode_bf16_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32], _sz),
     "qk4v8_attention_decode_bf16": ([_vp, _i32, _i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _vp,
                                      _i32, _i32, _f32, _i32, _vp, _sz, _vp, _vp, _vp, _vp], _i32),

@@ -1138,68 +1138,74 @@ int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, int n_new,
     return e == cudaSuccess ? QK4V8_OK : cuda_error(e, "kv append (rope) launch");
 }
 
-size_t qk4v8_decode_prefix_workspace_bytes(int B, int Hq, int nq, int prefix_splits, int num_splits) {
-    if (B <= 0 || Hq <= 0 || nq <= 0 || prefix_splits < 0 || num_splits < 0) return 0;
-    // The prefix's partials and log2-sum-exp, then the split kernel's workspace.
-    const size_t rows = static_cast<size_t>(B) * Hq * nq * prefix_splits;
-    return (rows * 129 * sizeof(float) + 15) / 16 * 16 + qk4v8_decode_workspace_bytes(B, Hq, nq, num_splits);
-}
+}  // extern "C"
 
-int qk4v8_decode_prefix_default_splits(int B, int Hq, int Hkv, int nq, int prefix_len) {
-    // `rows` of 128 query rows times `s` splits of the prefix's key tiles run in waves of
-    // one CTA per SM, each as long as its tiles plus a fixed cost (start, first loads,
-    // epilogue) of about kOverheadTiles; every split adds a partial result to join.
-    constexpr int kOverheadTiles = 5, kMaxSplits = 148;
-    if (B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || nq <= 0 || prefix_len <= 0) return 1;
+namespace {
+
+// How a shared-prefix decode is laid out (prefix.cu): every CTA takes an equal share of all
+// key tiles, and every (unit, share) may leave a partial result, units + shares in all.
+struct PrefixPlan {
+    int shares = 0, row_tiles = 0, tiles = 0, own = 0;
+    size_t o = 0, lse = 0, first = 0, last = 0, bytes = 0;  // workspace offsets
+};
+
+int plan_prefix(int B, int Hq, int Hkv, int nq, int prefix_len, int max_seqlen, PrefixPlan *plan) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || nq < 1 || nq > 8 || (Hq / Hkv) * nq > 128)
+        return set_error(QK4V8_ERR_INVALID_ARG, "need 1 <= nq <= 8 and (Hq/Hkv)*nq <= 128 (B=%d Hq=%d Hkv=%d nq=%d)", B,
+                         Hq, Hkv, nq);
+    if (prefix_len < 0 || max_seqlen < 0)
+        return set_error(QK4V8_ERR_INVALID_ARG, "bad lengths prefix_len=%d max_seqlen=%d", prefix_len, max_seqlen);
     int sms = 148, dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
         sms = 148;
         (void)cudaGetLastError();
     }
+    PrefixPlan q;
     const int64_t rows = static_cast<int64_t>(B) * (Hq / Hkv) * nq;
-    const int64_t units = (rows + 127) / 128 * Hkv;
-    const int tiles = (prefix_len + 127) / 128;
-    int best = 1;
-    int64_t best_cost = INT64_MAX;
-    for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
-        const int64_t waves = (units * s + sms - 1) / sms;
-        const int64_t cost = waves * ((tiles + s - 1) / s + kOverheadTiles);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = s;
-        }
-    }
-    return best;
+    const int64_t row_tiles = (rows + 127) / 128, units = row_tiles * Hkv;
+    // (Keys: a unit's tiles, of the prefix and of up to 129 sequences, are counted in an int.)
+    if (rows >= (int64_t{1} << 30) || units >= (int64_t{1} << 28) || static_cast<int64_t>(B) * Hq * nq >= (int64_t{1} << 31))
+        return set_error(QK4V8_ERR_INVALID_ARG, "too many query rows in one call");
+    q.row_tiles = static_cast<int>(row_tiles);
+    q.tiles = static_cast<int>((static_cast<int64_t>(prefix_len) + 127) / 128);
+    q.own = max_seqlen > 0;
+    // Every SM, unless there are fewer tiles than that even with all sequences at their longest.
+    const int64_t own_tiles = (static_cast<int64_t>(max_seqlen) + 127) / 128;
+    const int64_t most = q.tiles * units + own_tiles * 2 * B * Hkv + units;
+    q.shares = q.tiles || q.own ? static_cast<int>(most < sms ? most : sms) : 0;
+    const size_t slots = q.shares ? static_cast<size_t>(units) + q.shares : 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = q.bytes;
+        q.bytes += (bytes + 15) / 16 * 16;
+        return at;
+    };
+    q.o = take(slots * 128 * 128 * sizeof(float));
+    q.lse = take(slots * 128 * sizeof(float));
+    q.first = take(units * sizeof(int32_t));
+    q.last = take(units * sizeof(int32_t));
+    *plan = q;
+    return QK4V8_OK;
 }
-
-}  // extern "C"
-
-namespace {
 
 struct PrefixCache {
     const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
     int len, cap;                     // cap: contiguous cache
-    const int32_t *table = nullptr;   // pages of a pool
-    int num_pages = 0;
+    const int32_t *table;             // pages of a pool, or null
 };
 
 int decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq, int nq, int q_cap,
                   const PrefixCache &pre, const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
                   const uint8_t *v_scales, int Hkv, int kv_cap, const KvPages &pages, const int32_t *seqlens_k,
-                  int max_seqlen, int causal_in_block, float softmax_scale, int prefix_splits, int num_splits,
-                  void *workspace, size_t workspace_bytes, void *out, float *lse, int32_t *dev_status,
-                  cudaStream_t stream) {
+                  int max_seqlen, int causal_in_block, float softmax_scale, void *workspace, size_t workspace_bytes,
+                  void *out, float *lse, int32_t *dev_status, cudaStream_t stream) {
     int st;
+    PrefixPlan plan;
+    if ((st = plan_prefix(B, Hq, Hkv, nq, pre.len, max_seqlen, &plan))) return st;
     if (!out || !aligned16(out)) return set_error(QK4V8_ERR_INVALID_ARG, "out must be a 16-byte aligned pointer");
     if ((st = validate_packed(q_codes, q_scales, "Q"))) return st;
-    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || nq < 1 || nq > 8 || (Hq / Hkv) * nq > 128 ||
-        static_cast<int64_t>(B) * (Hq / Hkv) * nq >= (int64_t{1} << 30))
-        return set_error(QK4V8_ERR_INVALID_ARG, "bad sizes B=%d Hq=%d Hkv=%d nq=%d", B, Hq, Hkv, nq);
-    if (q_cap <= 0 || q_cap % 128 || pre.len < 0 || max_seqlen < 0 || prefix_splits < 0 || num_splits < 0)
-        return set_error(QK4V8_ERR_INVALID_ARG, "bad lengths or splits: q_cap=%d prefix_len=%d max_seqlen=%d", q_cap,
-                         pre.len, max_seqlen);
-    if (pre.len > 0) {
+    if (q_cap <= 0 || q_cap % 128) return set_error(QK4V8_ERR_INVALID_ARG, "bad q_cap %d", q_cap);
+    if (plan.tiles) {
         if ((st = validate_packed(pre.k_codes, pre.k_scales, "prefix K")) ||
             (st = validate_packed(pre.v_codes, pre.v_scales, "prefix V")))
             return st;
@@ -1207,92 +1213,95 @@ int decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq
             return set_error(QK4V8_ERR_INVALID_ARG, "prefix_cap must be a multiple of 128 and >= prefix_len (%d, %d)",
                              pre.cap, pre.len);
     }
-    const int tiles = (pre.len + 127) / 128;
-    const int psplits = tiles == 0          ? 0
-                        : prefix_splits > 0 ? (prefix_splits < tiles ? prefix_splits : tiles)
-                                            : qk4v8_decode_prefix_default_splits(B, Hq, Hkv, nq, pre.len);
-    const int splits = max_seqlen == 0  ? 0
-                       : num_splits > 0 ? num_splits
-                                        : qk4v8_decode_default_splits(B, Hq, Hkv, nq, max_seqlen);
-    const size_t need = qk4v8_decode_prefix_workspace_bytes(B, Hq, nq, psplits, splits);
-    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
-        return set_error(QK4V8_ERR_INVALID_ARG, "workspace must be 16-byte aligned and >= %zu bytes", need);
-    const size_t own_bytes = qk4v8_decode_workspace_bytes(B, Hq, nq, splits);
-    const size_t rows = static_cast<size_t>(B) * Hq * nq;
-    float *po = static_cast<float *>(workspace);
-    float *pl = po + rows * psplits * 128;
-    float *own = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + (need - own_bytes));
+    if (plan.own) {
+        if ((st = validate_packed(k_codes, k_scales, "K")) || (st = validate_packed(v_codes, v_scales, "V"))) return st;
+        if (!seqlens_k) return set_error(QK4V8_ERR_INVALID_ARG, "decode needs seqlens_k");
+        if (kv_cap <= 0 || kv_cap % 128 || max_seqlen > kv_cap ||
+            (!pages.block_table && static_cast<int64_t>(B) * Hkv * (kv_cap / 128) >= (int64_t{1} << 31)))
+            return set_error(QK4V8_ERR_INVALID_ARG, "bad lengths kv_cap=%d max_seqlen=%d", kv_cap, max_seqlen);
+    }
+    if (!workspace || !aligned16(workspace) || workspace_bytes < plan.bytes)
+        return set_error(QK4V8_ERR_INVALID_ARG, "workspace must be 16-byte aligned and >= %zu bytes", plan.bytes);
     if ((st = check_device())) return st;
     qk4v8::PrefixParams p{};
-    CUtensorMap tk;
-    if (psplits > 0) {
-        const int64_t row_tiles = (static_cast<int64_t>(B) * (Hq / Hkv) * nq + 127) / 128;
-        if (row_tiles * Hkv * psplits >= (int64_t{1} << 31))
-            return set_error(QK4V8_ERR_INVALID_ARG, "too many rows and splits");
-        if ((st = make_k_map(&tk, pre.k_codes, pre.table ? pre.num_pages * Hkv : Hkv, pre.table ? 128 : pre.cap)))
+    CUtensorMap pk, pv, k, v;
+    const bool paged = pages.block_table != nullptr;
+    if (plan.tiles) {
+        const int map_rows = paged ? pages.num_pages * Hkv : Hkv, map_cap = paged ? 128 : pre.cap;
+        if ((st = make_k_map(&pk, pre.k_codes, map_rows, map_cap)) ||
+            (st = make_v_map(&pv, pre.v_codes, map_rows, map_cap)))
             return st;
-        p.q_codes = q_codes;
-        p.q_scales = q_scales;
-        p.k_scales = pre.k_scales;
-        p.v_codes = pre.v_codes;
-        p.v_scales = pre.v_scales;
-        p.table = pre.table;
-        p.num_pages = pre.num_pages;
-        p.row_blocks = pre.table ? 1 : pre.cap / 128;
-        p.Hq = Hq;
-        p.Hkv = Hkv;
-        p.G = Hq / Hkv;
-        p.nq = nq;
-        p.q_cap = q_cap;
         p.len = pre.len;
-        p.tiles = tiles;
-        p.rows = B * p.G * nq;
-        p.row_tiles = static_cast<int>(row_tiles);
-        p.splits = psplits;
-        p.units = static_cast<int>(row_tiles * Hkv * psplits);
-        p.scale_log2 = resolve_scale(softmax_scale) * kLog2e;
-        p.ws_o = po;
-        p.ws_lse = pl;
-        p.status = dev_status;
-        p.test_stall = g_test_stall;
+        p.tiles = plan.tiles;
+        p.prefix_blocks = map_cap / 128;
+        p.p_k_scales = pre.k_scales;
+        p.p_v_scales = pre.v_scales;
+        p.prefix_table = pre.table;
     }
-    // The own keys first: its checks come before anything is enqueued.
-    if (splits > 0) {
-        int used = 0;
-        bool direct = false;
-        DecodeQuery q;
-        q.codes = q_codes;
-        q.scales = q_scales;
-        q.cap = q_cap;
-        if ((st = decode_splitkv(q, B, Hq, nq, k_codes, k_scales, v_codes, v_scales, Hkv, kv_cap, pages, seqlens_k,
-                                 max_seqlen, causal_in_block, 0, softmax_scale, splits, own, own_bytes, nullptr,
-                                 nullptr, dev_status, stream, &used, &direct)))
+    if (plan.own) {
+        const int map_rows = paged ? pages.num_pages * Hkv : B * Hkv, map_cap = paged ? 128 : kv_cap;
+        if ((st = make_k_map(&k, k_codes, map_rows, map_cap)) || (st = make_v_map(&v, v_codes, map_rows, map_cap)))
             return st;
+        p.own = 1;
+        // Lengths past max_seqlen are cut to it: no read behind the cache or its block table.
+        p.own_cap = max_seqlen;
+        p.own_blocks = map_cap / 128;
+        p.k_scales = k_scales;
+        p.v_scales = v_scales;
+        p.block_table = pages.block_table;
+        p.seqlens = seqlens_k;
+        p.max_pages = pages.max_pages;
     }
-    if (psplits > 0) {
-        const cudaError_t e = qk4v8::launch_prefix(tk, p, stream);
-        if (e != cudaSuccess) return cuda_error(e, "attention (prefix) launch");
-    }
-    const cudaError_t e = qk4v8::launch_prefix_merge(po, pl, psplits, own, own + rows * splits * 128, splits, B, Hq, nq,
-                                                     out, lse, stream);
-    return e == cudaSuccess ? QK4V8_OK : cuda_error(e, "prefix merge launch");
+    if (!plan.tiles) pk = k, pv = v;
+    if (!plan.own) k = pk, v = pv;
+    p.num_pages = pages.num_pages;
+    p.q_codes = q_codes;
+    p.q_scales = q_scales;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.nq = nq;
+    p.q_cap = q_cap;
+    p.gq = p.G * nq;
+    p.m_gq = static_cast<uint32_t>(((uint64_t{1} << 32) + p.gq - 1) / p.gq);
+    p.m_nq = static_cast<uint32_t>(((uint64_t{1} << 32) + nq - 1) / nq);
+    p.rows = B * p.gq;
+    p.row_tiles = plan.row_tiles;
+    p.scale_log2 = resolve_scale(softmax_scale) * kLog2e;
+    p.causal = causal_in_block ? 1 : 0;
+    p.shares = plan.shares;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.part_o = reinterpret_cast<float *>(ws + plan.o);
+    p.part_lse = reinterpret_cast<float *>(ws + plan.lse);
+    p.first = reinterpret_cast<int32_t *>(ws + plan.first);
+    p.last = reinterpret_cast<int32_t *>(ws + plan.last);
+    p.status = dev_status;
+    p.test_stall = g_test_stall;
+    const cudaError_t e = qk4v8::launch_prefix(pk, pv, k, v, p, out, lse, stream);
+    return e == cudaSuccess ? QK4V8_OK : cuda_error(e, "attention (prefix) launch");
 }
 
 }  // namespace
 
 extern "C" {
 
+size_t qk4v8_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int nq, int prefix_len, int max_seqlen) {
+    PrefixPlan plan;
+    return plan_prefix(B, Hq, Hkv, nq, prefix_len, max_seqlen, &plan) ? 0 : plan.bytes;
+}
+
 int qk4v8_attention_decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq, int nq, int q_cap,
                                   const uint8_t *p_k_codes, const uint8_t *p_k_scales, const uint8_t *p_v_codes,
                                   const uint8_t *p_v_scales, int prefix_len, int prefix_cap, const uint8_t *k_codes,
                                   const uint8_t *k_scales, const uint8_t *v_codes, const uint8_t *v_scales, int Hkv,
                                   int kv_cap, const int32_t *seqlens_k, int max_seqlen, int causal_in_block,
-                                  float softmax_scale, int prefix_splits, int num_splits, void *workspace,
-                                  size_t workspace_bytes, void *out, float *lse, int32_t *dev_status, void *stream) {
-    const PrefixCache pre{p_k_codes, p_k_scales, p_v_codes, p_v_scales, prefix_len, prefix_cap};
+                                  float softmax_scale, void *workspace, size_t workspace_bytes, void *out, float *lse,
+                                  int32_t *dev_status, void *stream) {
+    const PrefixCache pre{p_k_codes, p_k_scales, p_v_codes, p_v_scales, prefix_len, prefix_cap, nullptr};
     return decode_prefix(q_codes, q_scales, B, Hq, nq, q_cap, pre, k_codes, k_scales, v_codes, v_scales, Hkv, kv_cap,
-                         KvPages{}, seqlens_k, max_seqlen, causal_in_block, softmax_scale, prefix_splits, num_splits,
-                         workspace, workspace_bytes, out, lse, dev_status, static_cast<cudaStream_t>(stream));
+                         KvPages{}, seqlens_k, max_seqlen, causal_in_block, softmax_scale, workspace, workspace_bytes,
+                         out, lse, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 int qk4v8_attention_decode_prefix_paged(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq, int nq,
@@ -1300,24 +1309,20 @@ int qk4v8_attention_decode_prefix_paged(const uint8_t *q_codes, const uint8_t *q
                                         const uint8_t *v_codes, const uint8_t *v_scales, int Hkv, int num_pages,
                                         const int32_t *prefix_table, int prefix_len, const int32_t *block_table,
                                         int max_pages, const int32_t *seqlens_k, int max_seqlen, int causal_in_block,
-                                        float softmax_scale, int prefix_splits, int num_splits, void *workspace,
-                                        size_t workspace_bytes, void *out, float *lse, int32_t *dev_status,
-                                        void *stream) {
+                                        float softmax_scale, void *workspace, size_t workspace_bytes, void *out,
+                                        float *lse, int32_t *dev_status, void *stream) {
     if (!block_table || !prefix_table) return set_error(QK4V8_ERR_INVALID_ARG, "block_table or prefix_table is null");
     if (max_pages <= 0 || max_pages >= (1 << 24) || num_pages <= 0 || Hkv <= 0 ||
         static_cast<int64_t>(num_pages) * Hkv >= (int64_t{1} << 31))
         return set_error(QK4V8_ERR_INVALID_ARG, "bad page pool: num_pages=%d max_pages=%d", num_pages, max_pages);
-    PrefixCache pre{k_codes, k_scales, v_codes, v_scales, prefix_len, 0};
-    pre.table = prefix_table;
-    pre.num_pages = num_pages;
+    const PrefixCache pre{k_codes, k_scales, v_codes, v_scales, prefix_len, 0, prefix_table};
     KvPages pages;
     pages.block_table = block_table;
     pages.max_pages = max_pages;
     pages.num_pages = num_pages;
     return decode_prefix(q_codes, q_scales, B, Hq, nq, q_cap, pre, k_codes, k_scales, v_codes, v_scales, Hkv,
-                         max_pages * 128, pages, seqlens_k, max_seqlen, causal_in_block, softmax_scale, prefix_splits,
-                         num_splits, workspace, workspace_bytes, out, lse, dev_status,
-                         static_cast<cudaStream_t>(stream));
+                         max_pages * 128, pages, seqlens_k, max_seqlen, causal_in_block, softmax_scale, workspace,
+                         workspace_bytes, out, lse, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,14 +1,22 @@
-// Attention of a whole batch over the prefix that its sequences share.
+// Decode attention of a batch whose sequences share a prefix.
 //
-// With a shared prefix, the query rows of all B sequences that read one KV head
-// (B * G * nq of them) multiply the same keys, so decode over the prefix is a matrix
-// product again: each K/V tile is read once for 128 rows instead of once per
-// sequence. softmax over [prefix, own keys] splits into two partial results with
-// their log-sum-exp, which qk4v8_prefix_merge_kernel joins:
-//   O = sum_s 2^(lse_s - m) O_s / sum_s 2^(lse_s - m).
+// The query rows of all B sequences that read one KV head (B * G * nq of them)
+// multiply the same keys of the prefix, so there decode is a matrix product again:
+// each K/V tile is read once for 128 rows instead of once per sequence. After it
+// come each sequence's own keys, for its G * nq rows. Softmax over [prefix, own
+// keys] splits into partial results with their log-sum-exp, which the merge kernel
+// joins:  O = sum_s 2^(lse_s - m) O_s / sum_s 2^(lse_s - m).
 //
-// One CTA takes 128 query rows of a KV head (rows in (sequence, head, token) order,
-// gathered from the packed queries) against a split of the prefix, 128 keys a tile:
+// One persistent kernel does both. A unit is 128 query rows of a KV head (in (sequence,
+// head, token) order, gathered from the packed queries): first the prefix's keys, then
+// the own keys of each sequence that has rows among them, which the other rows do not
+// see (their warps skip them). So own keys cost no unit, no partial result and no
+// merge of their own: as units of one sequence each they took 6 us apiece, whatever
+// their length. The units' 128-key tiles, laid end to end (with one tile's time for a
+// unit's start and end), are cut into one equal share for each CTA; a unit that a
+// share's end cuts leaves several partial results. Piece (unit, share) has slot
+// unit + share, so the slots number units + shares whatever the lengths, which are on
+// the device: every CTA works its share out.
 //   S = Q K^T     kind::mxf4, E2M1 operands, the E8M0 scales read from TMEM.
 //   O += P V      kind::f16 on bf16 operands: P from TMEM, V expanded from E4M3.
 //
@@ -17,28 +25,35 @@
 // them. bf16 holds the same 8 significant bits in one conversion for two scores,
 // needs no block scale (its exponent takes p up to 2^64 above the reference), and
 // goes to TMEM without a swizzled store: about 3 instructions a score, so the
-// exponentials themselves (16 a clock and SM: 1024 clk a tile) become the bound.
-// V costs 2.3 instructions an element to expand, exactly (an E4M3 value times a
-// power of two has 4 significant bits), shared by the tile's 128 rows, on warps of
-// their own.
+// exponentials themselves (16 a clock and SM: 1024 clk a tile of 128 x 128) become
+// the bound. V costs 2.5 instructions an element to expand, exactly (an E4M3 value
+// times a power of two has 4 significant bits), on warps of their own.
 //
-// Softmax: two sets of four warps take alternate key tiles, one row per thread, all
-// 128 keys. P (64 columns) overwrites the front of S in the same buffer; S of tile i + 2 is issued behind P V of tile i, so the tensor
-// pipe's own order protects it. O has one reference per row, the row max of the
-// unit's first tile; p = 2^(s - m_O). It moves only when a later score passes it by
-// 2^64 (bf16 and fp32 keep their relative precision at any offset, so nothing is
-// gained by moving it sooner): the tile's owner then scales its row of O after the
-// P V before its own. The reference passes from a tile's owner to the next one's in
-// shared memory, right after the row max, well before the exponentials.
+// Softmax: three sets of four warps take turns on subtiles of 64 keys, one row per
+// thread. A set reads its S whole and frees the buffer at once, so the next S comes
+// while P is computed, and P V is on nobody's path. (P in the front of its own S
+// buffer, two sets on tiles of 128 keys: 2190 clk a tile of 128 x 128. Four sets of
+// 64 keys that hold S in TMEM until P is done: 2600, with 24 warps in each other's
+// way.)
+//
+// O has one reference per row, m_O, the row max of the unit's first subtile, and
+// p = 2^(s - m_O). It moves only when a score passes it by 2^64 (bf16 and fp32
+// keep their relative precision at any offset, so nothing is gained by moving it
+// sooner): the subtile's owner then scales its row of O after the P V before its own.
+// The reference passes from a subtile's owner to the next one's in shared memory,
+// right after the row max, well before the exponentials.
 // V carries a row of ones, so O column 128 sums P as rounded.
 //
-// Warp roles (512 threads): warps 0..7 softmax and epilogue, 8 K/V producer, 9 TMEM
-// allocator and MMA issuer, 10 query gather, 12..15 V expansion.
+// Warp roles (640 threads): warps 0..11 softmax and epilogue, 12 feeder (units, queries,
+// key tiles), 13 TMEM allocator and issuer of S, 14 issuer of D, 15 issuer of P V, 16..19 V
+// expansion. The softmax warps hold 64 scores and need 128 registers, the others 48
+// (384 * 128 + 256 * 48 = the 640 * 96 of the launch).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
+#include "../../include/qk4v8.h"
 #include "pipeline.cuh"
 #include "ptx.cuh"
 #include "qk4v8_internal.h"
@@ -48,14 +63,21 @@ namespace qk4v8 {
 
 namespace {
 
-constexpr int kPxKStages = 6;
+constexpr int kPxKStages = 4;
 constexpr int kPxVStages = 4;
-constexpr int kPxThreads = 512;
-constexpr int kPxProducerWarp = 8;
-constexpr int kPxMmaWarp = 9;
-constexpr int kPxQWarp = 10;
-constexpr int kPxExpandWarp = 12;
-constexpr float kPxMove = 64.0f;      // m_O moves once a score passes it by 2^64
+constexpr int kPxVSlots = 4;                // 64 tokens of expanded V each
+constexpr int kPxSets = 3;
+constexpr int kPxUnits = 8;                 // units announced at most
+constexpr int kPxTiles = 8;                 // tiles described at most
+constexpr int kPxSeqs = 132;                // sequences with rows among 128 consecutive ones: up to 129
+constexpr int kPxSoftmaxWarps = 4 * kPxSets;
+constexpr int kPxFeedWarp = kPxSoftmaxWarps;
+constexpr int kPxQkWarp = kPxFeedWarp + 1;
+constexpr int kPxDWarp = kPxFeedWarp + 2;
+constexpr int kPxPvWarp = kPxFeedWarp + 3;
+constexpr int kPxExpandWarp = kPxSoftmaxWarps + 4;
+constexpr int kPxThreads = 32 * (kPxExpandWarp + 4);
+constexpr float kPxMove = 64.0f;            // m_O moves once a score passes it by 2^64
 constexpr float kPxMaxMove = 65536.0f;
 
 struct PxSmem {
@@ -65,55 +87,104 @@ struct PxSmem {
     static constexpr int kK = kQ + 2 * kQBytes;                   // per stage: 128 keys x 64 B, 64-byte swizzle
     static constexpr int kVRows = 144;                            // 128 channels, the ones row, 15 zero rows
     static constexpr int kVHalf = kVRows * 128;                   // 64 tokens of bf16 per row
-    static constexpr int kVBytes = 2 * kVHalf;
-    static constexpr int kV = kK + kPxKStages * kKBytes;          // 2 buffers of bf16 V, 128-byte swizzle
+    static constexpr int kV = kK + kPxKStages * kKBytes;          // 4 slots of bf16 V, 128-byte swizzle
     static constexpr int kRawBytes = 128 * 128;
-    static constexpr int kRaw = kV + 2 * kVBytes;                 // per stage: E4M3 block, channel rows
-    static constexpr int kSfQ = kRaw + kPxVStages * kRawBytes;    // 512-byte scale atoms
+    static constexpr int kRaw = kV + kPxVSlots * kVHalf;          // per stage: E4M3 block, 128-byte swizzle
+    static constexpr int kUnit = kRaw + kPxVStages * kRawBytes;   // 32 x 32 unit matrix, E4M3, 128-byte swizzle
+    static constexpr int kSfQ = kUnit + 32 * 128;                 // 512-byte scale atoms
     static constexpr int kSfK = kSfQ + 2 * 512;
     static constexpr int kSfV = kSfK + kPxKStages * 512;
-    static constexpr int kRef = kSfV + kPxVStages * 512;          // float [2][128]: m_O by tile parity
-    static constexpr int kBar = kRef + 2 * 128 * 4;
-    // k_full/k_empty, raw_full/raw_empty per stage; v_full/v_empty per bf16 buffer;
-    // q_full/q_empty per Q buffer; s_full, p_full, pv_done per set; o_full, o_free,
-    // drain; reference [4 quarters][2].
-    static constexpr int kNumBars = 2 * kPxKStages + 2 * kPxVStages + 4 + 4 + 6 + 3 + 8;
-    static constexpr int kMisc = kBar + kNumBars * 8;
-    static constexpr int kUsed = kMisc + 16;
+    static constexpr int kSfOne = kSfV + kPxVStages * 512;
+    static constexpr int kRef = kSfOne + 512;                     // float [128]: m_O of each row
+    static constexpr int kBar = kRef + 128 * 4;
+    // Barriers (byte offsets).
+    static constexpr int kKFull = kBar, kKEmpty = kKFull + 8 * kPxKStages;             // per stage
+    static constexpr int kRawFull = kKEmpty + 8 * kPxKStages;                          // per stage
+    static constexpr int kRawEmpty = kRawFull + 8 * kPxVStages;
+    static constexpr int kDFull = kRawEmpty + 8 * kPxVStages, kDFree = kDFull + 8;
+    static constexpr int kVFull = kDFree + 8, kVEmpty = kVFull + 8 * kPxVSlots;        // per slot
+    static constexpr int kQFull = kVEmpty + 8 * kPxVSlots, kQEmpty = kQFull + 16;      // per Q buffer
+    static constexpr int kSFull = kQEmpty + 16, kSFree = kSFull + 8 * kPxSets;         // per set
+    static constexpr int kPFull = kSFree + 8 * kPxSets, kPvDone = kPFull + 8 * kPxSets;
+    static constexpr int kOFull = kPvDone + 8 * kPxSets, kOFree = kOFull + 8, kDrain = kOFree + 8;
+    static constexpr int kRefBar = kDrain + 8;                                         // [quarter][set]
+    static constexpr int kUnitFull = kRefBar + 8 * 4 * kPxSets, kUnitEmpty = kUnitFull + 8 * kPxUnits;
+    static constexpr int kBarEnd = kUnitEmpty + 8 * kPxUnits;
+    static constexpr int kMisc = (kBarEnd + 15) / 16 * 16;  // TMEM address, abort flag
+    static constexpr int kUnits = kMisc + 16;          // PxUnit [kPxUnits]
+    static constexpr int kTiles = kUnits + 64 * kPxUnits;   // PxTile [kPxTiles]
+    static constexpr int kLens = kTiles + 8 * kPxTiles;     // int [kPxSeqs]: the unit's sequences
+    static constexpr int kUsed = kLens + 4 * kPxSeqs;
     static constexpr int kBytes = kUsed + 1024;
 };
-static_assert(PxSmem::kK % 1024 == 0 && PxSmem::kV % 1024 == 0 && PxSmem::kVHalf % 1024 == 0,
+static_assert(PxSmem::kK % 1024 == 0 && PxSmem::kV % 1024 == 0 && PxSmem::kVHalf % 1024 == 0 &&
+                  PxSmem::kRaw % 1024 == 0 && PxSmem::kUnit % 1024 == 0,
               "swizzled tiles need 1024-byte alignment");
-static_assert(PxSmem::kBar % 8 == 0 && PxSmem::kRaw % 16 == 0, "alignment");
+static_assert(PxSmem::kBar % 8 == 0 && PxSmem::kSfQ % 128 == 0, "alignment");
 static_assert(PxSmem::kBytes <= 227 * 1024, "shared memory budget");
 
 constexpr uint32_t kPxTmemCols = 512;
-constexpr uint32_t kPxColO = 256;  // 144 columns
-__device__ __forceinline__ uint32_t px_col_s(int set) { return 128u * set; }  // P in its first 64 columns
-__device__ __forceinline__ uint32_t px_col_sf_q(int qb) { return 400u + 4u * qb; }
-__device__ __forceinline__ uint32_t px_col_sf_k(int set) { return 408u + 4u * set; }
+// S 3 x 64, D (V as the tensor core expands it) 64, O 144, P 3 x 32, scales: all 512.
+constexpr uint32_t kPxColD = 192, kPxColO = 256, kPxColSfQ = 496, kPxColSfK = 500, kPxColSfV = 504, kPxColOne = 508;
+__device__ __forceinline__ uint32_t px_col_s(int set) { return 64u * set; }
+__device__ __forceinline__ uint32_t px_col_p(int set) { return 400u + 32u * set; }
 
-// Block-scaled E2M1 x E2M1, N = 128 keys; bf16 x bf16 into fp32, N = 144.
-constexpr uint32_t kPxIdQK = (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+// Block-scaled E2M1 x E2M1, N = 64 keys; block-scaled E4M3 x E4M3, N = 32; bf16 x bf16, N = 144.
+constexpr uint32_t kPxIdQK = (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+constexpr uint32_t kPxIdD = ((32u >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
 constexpr uint32_t kPxIdPV =
     (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t(PxSmem::kVRows) >> 3) << 17) | ((128u >> 4) << 24);
-__device__ __forceinline__ uint32_t px_sf_id(uint32_t idesc, uint32_t id) { return idesc | (id << 29) | (id << 4); }
+constexpr __host__ __device__ uint32_t px_sf_id(uint32_t idesc, uint32_t id) { return idesc | (id << 29) | (id << 4); }
+
+// The issuing threads' code is short on purpose: at about 7 clk an instruction, what they
+// execute between two products is what the products wait for. So barriers go by their
+// shared-memory address and descriptors by their low word (the high one is constant).
+constexpr uint32_t px_desc_hi(uint32_t sbo, uint32_t layout) { return (sbo >> 4) | (1u << 14) | (layout << 29); }
+constexpr uint32_t kHi64B = px_desc_hi(512, 4), kHi128B = px_desc_hi(1024, 2), kHiAtom = px_desc_hi(128, 0);
+__device__ __forceinline__ uint32_t px_desc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | (lbo << 12); }
 
 // D[128, N] (+)= A B, A bf16 in TMEM (two K elements a column), B bf16 in shared memory.
-__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
+template <bool kFirst>
+__device__ __forceinline__ void px_mma_bf16(uint32_t d, uint32_t a, uint32_t blo, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(blo), "n"(kHi128B), "n"(kPxIdPV), "r"(kFirst ? accumulate : 1u)
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
+// Block-scaled products, K = 64 of E2M1 and K = 32 of E4M3, `id` the scales' byte.
+template <uint32_t kIdesc>
+__device__ __forceinline__ void px_mma_mxf4(uint32_t d, uint32_t alo, uint32_t blo, uint32_t sfa, uint32_t sfb,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "n"(kHi64B), "n"(kIdesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void px_mma_mxf8(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "n"(kHi128B), "r"(idesc), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+__device__ __forceinline__ void px_cp_atom(uint32_t taddr, uint32_t lo) {
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(lo), "n"(kHiAtom)
+        : "memory");
+}
+__device__ __forceinline__ void px_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void px_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
@@ -126,10 +197,9 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 __device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 // One elected thread of the (converged) warp.
@@ -139,43 +209,228 @@ __device__ __forceinline__ bool elect_one() {
     return pred != 0;
 }
 
+// One look at an mbarrier phase.
+__device__ __forceinline__ bool px_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait on an mbarrier phase: false past kWaitTimeoutNs, or once the CTA's abort flag is
+// up. A role whose wait gave up raises the flag at its end (px_give_up), so the others
+// follow at once. A dozen instructions, all of them: with waits of sixty at thirty
+// places the roles' loops left the SM's instruction cache (103 misses a tile, and every
+// instruction of a softmax warp took 15 clk). No time hint either: with one, a try sleeps
+// well past the barrier's completion.
+__device__ __forceinline__ bool px_wait(uint32_t bar, uint32_t parity, uint32_t flag) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t1;\n\t.reg .b32 f;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra PX_DONE;\n\t"
+        "mov.u64 t0, %%globaltimer;\n\t"
+        "PX_AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra PX_DONE;\n\t"
+        "ld.volatile.shared.b32 f, [%3];\n\t"
+        "mov.u64 t1, %%globaltimer;\n\t"
+        "sub.u64 t1, t1, t0;\n\t"
+        "setp.gt.u64 q, t1, %4;\n\t"
+        "setp.ne.or.b32 q, f, 0, q;\n\t"
+        "@!q bra PX_AGAIN;\n\t"
+        "PX_DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(flag), "n"(kWaitTimeoutNs)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void px_give_up(volatile uint32_t *flag, int32_t *status) {
+    if (*flag) return;
+    *flag = 1;
+    if (status) atomicCAS(status, 0, QK4V8_ERR_TIMEOUT);
+}
+
+// O *= 2^-E for the row (rescale_o_lane without the call).
+__device__ __forceinline__ void px_rescale(uint32_t taddr, int E) {
+    const float a = E < 126 ? __uint_as_float(static_cast<uint32_t>(127 - E) << 23) : 0.f;
+#pragma unroll 1
+    for (int c = 0; c < PxSmem::kVRows; c += 4) {
+        uint32_t o[4];
+        tc_ld_32x32b_x4(taddr + c, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+        tc_st_32x32b_x4(taddr + c, o);
+    }
+    tc_wait_st();
+}
+
+// ------------------------------------------------------------------ schedule
+
+constexpr int kPxUnitCost = 1;  // a unit's start and end, in tiles
+
+// Sequence b's own keys.
+__device__ __forceinline__ int px_own_len(const PrefixParams &p, int b) {
+    return p.own ? imax(0, imin(p.seqlens[b], p.own_cap)) : 0;
+}
+
+// n / d for 0 <= n < 2^30, 1 <= d <= 128, with m = ceil(2^32 / d): the product's high word is the
+// quotient or one more. (A division by a variable is some forty instructions; the feeder's
+// two for each query row took 12 us a unit.)
+__device__ __forceinline__ int px_div(int n, int d, uint32_t m) {
+    if (d == 1) return n;  // 2^32 does not fit m
+    const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(n), m));
+    return q - (q * d > n ? 1 : 0);
+}
+
+// Sequences with rows in row tile qt.
+__device__ __forceinline__ int px_seq_lo(const PrefixParams &p, int qt) { return px_div(qt * 128, p.gq, p.m_gq); }
+__device__ __forceinline__ int px_seq_hi(const PrefixParams &p, int qt) {
+    return px_div(imin(qt * 128 + 128, p.rows) - 1, p.gq, p.m_gq);
+}
+
+// Tiles of a unit of row tile qt and its cost (0: no key at all).
+__device__ __forceinline__ int px_span(int tiles) { return tiles > 0 ? tiles + kPxUnitCost : 0; }
+
+// A unit's piece in the share, announced in shared memory to all roles (T = 0: no more).
 struct PxUnit {
-    int h, q0, split, t0, T;  // KV head, first row, split, its first key tile and count
+    int qt, h;       // row tile and KV head
+    int row0, rows;  // its rows: row0 .. row0 + rows - 1 of the KV head
+    int t0, T;       // first key tile and count
+    int edge;        // 1: the piece has the unit's first tile, 2: its last one
+};
+static_assert(sizeof(PxUnit) <= 64, "an entry of the announced units");
+
+// A key tile, described in shared memory by the feeder as it loads it.
+struct PxTile {
+    int rows;  // rows that see it: first | (last + 1) << 8; own keys: | 1 << 16
+    int keys;  // keys from the tile's first on
 };
 
-// Units that run side by side share a split's keys (consecutive row tiles).
-__device__ __forceinline__ PxUnit px_unit(const PrefixParams &p, int idx) {
-    PxUnit u;
-    const int qt = idx % p.row_tiles;
-    idx /= p.row_tiles;
-    u.h = idx % p.Hkv;
-    u.split = idx / p.Hkv;
-    u.q0 = qt * 128;
-    u.t0 = static_cast<int>(static_cast<int64_t>(u.split) * p.tiles / p.splits);
-    u.T = static_cast<int>(static_cast<int64_t>(u.split + 1) * p.tiles / p.splits) - u.t0;
-    return u;
+// Steps through the units with a tile in this CTA's share. The whole warp calls it.
+struct PxIter {
+    int left, qt, h, off;  // cost left in the share; unit, and how far into it
+    int tiles;             // key tiles of the units of row tile qt
+    __device__ __forceinline__ static int count(const PrefixParams &p, int qt, int lane) {
+        int n = 0;
+        if (p.own) {
+            for (int b = px_seq_lo(p, qt) + lane; b <= px_seq_hi(p, qt); b += 32) n += (px_own_len(p, b) + 127) >> 7;
+            n = __reduce_add_sync(0xffffffffu, n);
+        }
+        return p.tiles + n;
+    }
+    __device__ __forceinline__ void begin(const PrefixParams &p, int lane) {
+        // The cost of row tile qt's units: a lane each (loads in flight together), or, of a few
+        // row tiles, by the warp.
+        auto cost = [&](int qt) -> int64_t {
+            if (qt >= p.row_tiles) return 0;
+            int n = p.tiles;
+            if (p.own) {
+                const int b1 = px_seq_hi(p, qt);
+#pragma unroll 8
+                for (int b = px_seq_lo(p, qt); b <= b1; ++b) n += (px_own_len(p, b) + 127) >> 7;
+            }
+            return static_cast<int64_t>(px_span(n)) * p.Hkv;
+        };
+        const bool few = p.row_tiles <= 8;
+        int64_t mine = 0, kept = 0;  // kept: lane i's, of row tile i
+        if (few) {
+            for (int q = 0; q < p.row_tiles; ++q) {
+                const int64_t v = static_cast<int64_t>(px_span(count(p, q, lane))) * p.Hkv;
+                if (lane == q) kept = mine = v;
+            }
+        } else {
+            for (int q = lane; q < p.row_tiles; q += 32) mine += cost(q);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        const int64_t w = mine;
+        const int64_t share = (w + gridDim.x - 1) / gridDim.x;
+        int64_t r = blockIdx.x * share;
+        left = r < w ? static_cast<int>(share < w - r ? share : w - r) : 0;
+        qt = h = off = tiles = 0;
+        if (left == 0) return;
+        for (int q0 = 0;; q0 += 32) {  // ends: r < w
+            int64_t c = few ? kept : cost(q0 + lane);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, c, o);
+                if (lane >= o) c += v;
+            }
+            const int k = __popc(__ballot_sync(0xffffffffu, c <= r));  // row tile q0 + k holds r
+            const int64_t before = __shfl_sync(0xffffffffu, c, k > 0 ? k - 1 : 0);
+            if (k > 0) r -= before;
+            if (k < 32 || q0 + 32 >= p.row_tiles) {
+                qt = q0 + (k < 32 ? k : 31);
+                break;
+            }
+        }
+        tiles = count(p, qt, lane);
+        const int span = imax(1, px_span(tiles));
+        h = static_cast<int>(r / span);
+        off = static_cast<int>(r - static_cast<int64_t>(h) * span);
+    }
+    __device__ __forceinline__ bool next(const PrefixParams &p, int lane, PxUnit &u) {
+        while (left > 0 && qt < p.row_tiles) {
+            const int span = px_span(tiles);
+            const int take = imin(left, span - off);
+            const int lo = imax(off - kPxUnitCost, 0), hi = off + take - kPxUnitCost;
+            u.qt = qt;
+            u.h = h;
+            u.row0 = qt * 128;
+            u.rows = imin(128, p.rows - u.row0);
+            u.t0 = lo;
+            u.T = hi - lo;
+            u.edge = (lo == 0 ? 1 : 0) | (hi == tiles ? 2 : 0);
+            left -= take;
+            off = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                if (++qt < p.row_tiles) tiles = count(p, qt, lane);
+            }
+            if (hi > lo) return true;
+        }
+        u.T = 0;
+        return false;
+    }
+};
+
+// Row n of KV head h: its query head of [B][Hq] and token.
+__device__ __forceinline__ int64_t px_row(const PrefixParams &p, int h, int n, int &t) {
+    const int b = px_div(n, p.gq, p.m_gq);
+    const int r = n - b * p.gq;
+    const int g = px_div(r, p.nq, p.m_nq);
+    t = r - g * p.nq;
+    return static_cast<int64_t>(b) * p.Hq + h * p.G + g;
 }
 
-// Row n of KV head h: query head, sequence and token; returns the row of [B][Hq][nq].
-__device__ __forceinline__ int64_t px_row(const PrefixParams &p, int h, int n, int64_t &bh, int &t) {
-    t = n % p.nq;
-    const int bg = n / p.nq;
-    const int b = bg / p.G;
-    bh = static_cast<int64_t>(b) * p.Hq + h * p.G + (bg - b * p.G);
-    return bh * p.nq + t;
+// Asynchronous copies into shared memory; zeros where there is nothing to copy.
+__device__ __forceinline__ void px_copy16(uint32_t dst, const void *src, bool any) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(any ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void px_copy4(uint32_t dst, const void *src, bool any) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(any ? 4 : 0) : "memory");
 }
 
-// The prefix's tile `tile` of head h: row and block of the K/V arrays. A page outside
-// the pool reads page 0 and is reported.
-__device__ __forceinline__ void px_tile(const PrefixParams &p, int h, int tile, int &row, int &blk) {
-    if (!p.table) {
-        row = h;
+// Key tile `tile` of the prefix (seq < 0) or of a sequence's own keys: row and block of the
+// K/V arrays. A page outside the pool reads page 0 and is reported.
+__device__ __forceinline__ void px_tile(const PrefixParams &p, int h, int seq, int tile, int &row, int &blk) {
+    const int32_t *table = seq < 0 ? p.prefix_table : p.block_table;
+    if (!table) {
+        row = seq < 0 ? h : seq * p.Hkv + h;
         blk = tile;
         return;
     }
-    int page = p.table[tile];
+    int page = seq < 0 ? table[tile] : table[static_cast<int64_t>(seq) * p.max_pages + tile];
     if (page < 0 || page >= p.num_pages) {
-        if (p.status) atomicCAS(p.status, 0, 1);
+        if (p.status) atomicCAS(p.status, 0, QK4V8_ERR_INVALID_ARG);
         page = 0;
     }
     row = page * p.Hkv + h;
@@ -185,519 +440,709 @@ __device__ __forceinline__ void px_tile(const PrefixParams &p, int h, int tile, 
 }  // namespace
 
 __global__ void __launch_bounds__(kPxThreads, 1)
-    qk4v8_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ PrefixParams p) {
+    qk4v8_prefix_kernel(const __grid_constant__ CUtensorMap tmap_pk, const __grid_constant__ CUtensorMap tmap_pv,
+                        const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                        const __grid_constant__ PrefixParams p) {
     using S = PxSmem;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBar);
-    uint64_t *k_full = bars;
-    uint64_t *k_empty = k_full + kPxKStages;
-    uint64_t *raw_full = k_empty + kPxKStages;
-    uint64_t *raw_empty = raw_full + kPxVStages;
-    uint64_t *v_full = raw_empty + kPxVStages;  // [bf16 buffer]
-    uint64_t *v_empty = v_full + 2;
-    uint64_t *q_full = v_empty + 2;             // [Q buffer]
-    uint64_t *q_empty = q_full + 2;
-    uint64_t *s_full = q_empty + 2;             // [set]
-    uint64_t *p_full = s_full + 2;              // [set]
-    uint64_t *pv_done = p_full + 2;             // [set]
-    uint64_t *o_full = pv_done + 2;
-    uint64_t *o_free = o_full + 1;
-    uint64_t *drain = o_free + 1;
-    uint64_t *ref_bar = drain + 1;              // [quarter][tile parity]
+    const uint32_t sb = smem_u32(smem);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + S::kMisc + 4);
+    const uint32_t flag = sb + S::kMisc + 4;
+    auto wait = [&](uint32_t offset, uint32_t parity) { return px_wait(sb + offset, parity, flag); };
+    auto wait_warp = [&](uint32_t offset, uint32_t parity) { return __all_sync(0xffffffffu, wait(offset, parity)) != 0; };
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kPxKStages; ++s) {
-            mbar_init(&k_full[s], 1);
-            mbar_init(&k_empty[s], 1);
-        }
-        for (int s = 0; s < kPxVStages; ++s) {
-            mbar_init(&raw_full[s], 1);
-            mbar_init(&raw_empty[s], 4);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&v_full[s], 4);
-            mbar_init(&v_empty[s], 1);
-            mbar_init(&q_full[s], 1);
-            mbar_init(&q_empty[s], 1);
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 4);
-            mbar_init(&pv_done[s], 1);
-        }
-        mbar_init(o_full, 1);
-        mbar_init(o_free, 8);
-        mbar_init(drain, 1);
-        for (int g = 0; g < 8; ++g) mbar_init(&ref_bar[g], 1);
+    if (threadIdx.x == 32) {
+        auto init = [&](int offset, int n, uint32_t count) {
+            for (int i = 0; i < n; ++i) mbar_init(reinterpret_cast<uint64_t *>(smem + offset + 8 * i), count);
+        };
+        init(S::kKFull, kPxKStages, 1);
+        init(S::kKEmpty, kPxKStages, 1);
+        init(S::kRawFull, kPxVStages, 1);
+        init(S::kRawEmpty, kPxVStages, 1);
+        init(S::kDFull, 1, 1);
+        init(S::kDFree, 1, 4);
+        init(S::kVFull, kPxVSlots, 4);
+        init(S::kVEmpty, kPxVSlots, 1);
+        init(S::kQFull, 2, 1);
+        init(S::kQEmpty, 2, 1);
+        init(S::kSFull, kPxSets, 1);
+        init(S::kSFree, kPxSets, 4);
+        init(S::kPFull, kPxSets, 4);
+        init(S::kPvDone, kPxSets, 1);
+        init(S::kOFull, 1, 1);
+        init(S::kOFree, 1, kPxSoftmaxWarps);
+        init(S::kDrain, 1, 3);
+        init(S::kRefBar, 4 * kPxSets, 1);
+        init(S::kUnitFull, kPxUnits, 1);
+        // The three issuers, the expanding and the softmax warps.
+        init(S::kUnitEmpty, kPxUnits, 3 + 4 + kPxSoftmaxWarps);
         // A status already set by another launch or CTA: unwind at once, uniformly.
         *abort_flag = (p.status && *reinterpret_cast<const volatile int32_t *>(p.status) != 0) ? 1u : 0u;
         fence_barrier_init();
     }
-    if (warp == kPxMmaWarp) {
+    if (threadIdx.x == 32 * kPxFeedWarp) {
+        prefetch_tensormap(&tmap_pk);
+        prefetch_tensormap(&tmap_pv);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+    }
+    if (warp == kPxQkWarp) {
         tmem_alloc(tmem_slot, kPxTmemCols);
         tmem_relinquish();
     }
     if (warp >= kPxExpandWarp) {
-        // Constant rows of both V buffers: row 128 = 1.0, rows 129..143 = 0.
-        for (int i = threadIdx.x - 32 * kPxExpandWarp; i < 2 * 2 * 16 * 8; i += 128) {
-            const int half = i >> 7, r = (i >> 3) & 15;
+        // Constant rows of the V slots (row 128 = 1.0, rows 129..143 = 0), the unit matrix
+        // (E4M3 1.0 is 0x38) and the scales of 2^0.
+        const int tid = threadIdx.x - 32 * kPxExpandWarp;
+        for (int i = tid; i < kPxVSlots * 16 * 8; i += 128) {
+            const int slot = i >> 7, r = (i >> 3) & 15;
             const uint32_t v = r == 0 ? 0x3F803F80u : 0u;
-            *reinterpret_cast<uint4 *>(smem + S::kV + half * S::kVHalf + (128 + r) * 128 + (i & 7) * 16) =
+            *reinterpret_cast<uint4 *>(smem + S::kV + slot * S::kVHalf + (128 + r) * 128 + (i & 7) * 16) =
                 make_uint4(v, v, v, v);
         }
+        for (int i = tid; i < 32 * 8; i += 128) {
+            const int r = i >> 3, at = (i & 7) ^ (r & 7);  // row r's 16-byte chunk `at`
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            if (at == r >> 4) w[(r >> 2) & 3] = 0x38u << (8 * (r & 3));
+            *reinterpret_cast<uint4 *>(smem + S::kUnit + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (tid < 32) reinterpret_cast<uint4 *>(smem + S::kSfOne)[tid] =
+            make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // The announced units: unit c's entry once it is there, and its release.
+    auto unit_at = [&](int c) { return reinterpret_cast<const PxUnit *>(smem + S::kUnits + 64 * (c & (kPxUnits - 1))); };
+    auto unit_wait = [&](int c) { return wait(S::kUnitFull + 8 * (c & (kPxUnits - 1)), (c / kPxUnits) & 1); };
+    auto unit_done = [&](int c) { px_arrive(sb + S::kUnitEmpty + 8 * (c & (kPxUnits - 1))); };
 
-    if (warp == kPxProducerWarp) {
-        // ------------------------------------------------------------- K/V producer
-        if (elect_one()) {
-            prefetch_tensormap(&tmap_k);
-            int g = 0;                   // tiles so far
-            int k_issued = 0, v_issued = 0;
-            bool ok = true;
-            for (int un = blockIdx.x; un < p.units && ok; un += gridDim.x) {
-                const PxUnit u = px_unit(p, un);
-                int row, blk;
-                px_tile(p, u.h, u.t0, row, blk);
-                for (int i = 0; i < u.T; ++i) {
-                    int nrow = 0, nblk = 0;
-                    if (i + 1 < u.T) px_tile(p, u.h, u.t0 + i + 1, nrow, nblk);  // ahead of the waits
-                    const int gi = g + i;
-                    const int st = gi % kPxKStages, sv = gi % kPxVStages;
-                    const int64_t at = static_cast<int64_t>(row) * p.row_blocks + blk;
-                    ok = wait_bar(&k_empty[st], ((gi / kPxKStages) & 1) ^ 1, abort_flag, p.status);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&k_full[st], S::kKBytes + 512);
-                    tma_load_3d(smem + S::kK + st * S::kKBytes, &tmap_k, 0, blk * 128, row, &k_full[st]);
-                    bulk_load(smem + S::kSfK + st * 512, p.k_scales + at * 512, 512, &k_full[st]);
-                    k_issued = gi + 1;
-                    ok = wait_bar(&raw_empty[sv], ((gi / kPxVStages) & 1) ^ 1, abort_flag, p.status);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&raw_full[sv], S::kRawBytes + 512);
-                    bulk_load(smem + S::kRaw + sv * S::kRawBytes, p.v_codes + at * S::kRawBytes, S::kRawBytes,
-                              &raw_full[sv]);
-                    bulk_load(smem + S::kSfV + sv * 512, p.v_scales + at * 512, 512, &raw_full[sv]);
-                    v_issued = gi + 1;
-                    row = nrow;
-                    blk = nblk;
-                }
-                g += u.T;
-            }
-            // Let every issued copy land before the CTA can retire.
-            auto settle = [&](uint64_t *bar, uint32_t parity) {
-                const uint64_t t0 = globaltimer_ns();
-                while (!mbar_try_wait(bar, parity))
-                    if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
-            };
-            for (int i = imax(0, k_issued - kPxKStages); i < k_issued; ++i)
-                settle(&k_full[i % kPxKStages], (i / kPxKStages) & 1);
-            for (int i = imax(0, v_issued - kPxVStages); i < v_issued; ++i)
-                settle(&raw_full[i % kPxVStages], (i / kPxVStages) & 1);
-        }
-        __syncwarp();
-    } else if (warp == kPxQWarp) {
-        // ------------------------------------------------------------- query gather
-        int c = 0;  // units so far
-        for (int un = blockIdx.x; un < p.units; un += gridDim.x, ++c) {
-            const PxUnit u = px_unit(p, un);
-            const int qb = c & 1;
-            if (!__all_sync(0xffffffffu, wait_bar(&q_empty[qb], ((c >> 1) & 1) ^ 1, abort_flag, p.status))) break;
-            uint8_t *qbuf = smem + S::kQ + qb * S::kQBytes;
-            uint8_t *sfq = smem + S::kSfQ + qb * 512;
-            // Rows lane / 4 + 8 i, 16-byte chunk lane % 4: four loads of a lane in flight.
-#pragma unroll 1
-            for (int i0 = 0; i0 < 16; i0 += 4) {
-                uint4 code[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int n = u.q0 + (lane >> 2) + 8 * (i0 + i);
-                    code[i] = make_uint4(0, 0, 0, 0);
-                    if (n < p.rows) {
-                        int64_t bh;
-                        int t;
-                        px_row(p, u.h, n, bh, t);
-                        code[i] = *reinterpret_cast<const uint4 *>(p.q_codes + (bh * p.q_cap + t) * 64 + (lane & 3) * 16);
-                    }
-                }
-                const int rs = u.q0 + lane + 8 * i0;  // scale word of row lane + 32 (i0 / 4)
-                uint32_t sf = 0;
-                if (rs < p.rows) {
-                    int64_t bh;
-                    int t;
-                    px_row(p, u.h, rs, bh, t);
-                    sf = *reinterpret_cast<const uint32_t *>(p.q_scales + bh * (p.q_cap / 128) * 512 + t * 16);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = (lane >> 2) + 8 * (i0 + i);
-                    *reinterpret_cast<uint4 *>(qbuf + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)) = code[i];
-                }
-                *reinterpret_cast<uint32_t *>(sfq + lane * 16 + i0) = sf;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && !(p.test_stall && c == 0)) mbar_arrive(&q_full[qb]);
-        }
-    } else if (warp == kPxMmaWarp) {
-        // -------------------------------------------------------------- MMA issuer
-        if (elect_one()) {
-            const uint32_t sb = smem_u32(smem);
-            const uint64_t dQ0 = smem_desc(sb + S::kQ, 16, 512, 4);
-            const uint64_t dK0 = smem_desc(sb + S::kK, 16, 512, 4);
-            const uint64_t dV0 = smem_desc(sb + S::kV, 16, 1024, 2);
-            const uint64_t dSfQ0 = smem_desc(sb + S::kSfQ, 0, 128, 0);
-            const uint64_t dSfK0 = smem_desc(sb + S::kSfK, 0, 128, 0);
-            const uint32_t tO = tmem + kPxColO;
-            bool ok = true;
-            int g = 0, c = 0;
-            for (int un = blockIdx.x; un < p.units && ok; un += gridDim.x) {
-                const int T = px_unit(p, un).T;
-                const int qb = c & 1;
-                ok = wait_bar(&q_full[qb], (c >> 1) & 1, abort_flag, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t tSfQ = tmem + px_col_sf_q(qb);
-                const uint64_t dQ = dQ0 + static_cast<uint64_t>(qb * (S::kQBytes >> 4));
-                tc_cp_32x128b_warpx4(tSfQ, dSfQ0 + static_cast<uint64_t>(qb * 32));
-                // S(gi) into buffer gi & 1: behind P V(gi - 2) in the tensor pipe, and the
-                // warps read S(gi - 2) before they wrote that P.
-                auto issue_qk = [&](int i) -> bool {
-                    const int gi = g + i, st = gi % kPxKStages;
-                    if (!wait_bar(&k_full[st], (gi / kPxKStages) & 1, abort_flag, p.status)) return false;
-                    tc_fence_after();
-                    const uint32_t tSfK = tmem + px_col_sf_k(gi & 1), tS = tmem + px_col_s(gi & 1);
-                    const uint64_t dK = dK0 + static_cast<uint64_t>(st * (S::kKBytes >> 4));
-                    tc_cp_32x128b_warpx4(tSfK, dSfK0 + static_cast<uint64_t>(st * 32));
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        tc_mma_mxf4(tS, dQ + 2 * k, dK + 2 * k, px_sf_id(kPxIdQK, 2 * k), tSfQ | ((2u * k) << 30),
-                                    tSfK | ((2u * k) << 30), k > 0 ? 1u : 0u);
-                    tc_commit(&s_full[gi & 1]);
-                    tc_commit(&k_empty[st]);
-                    return true;
-                };
-                auto issue_pv = [&](int i) -> bool {
-                    const int gi = g + i, vb = gi & 1;
-                    if (!wait_bar(&v_full[vb], (gi >> 1) & 1, abort_flag, p.status)) return false;
-                    if (i == 0 && c >= 1 && !wait_bar(o_free, (c - 1) & 1, abort_flag, p.status)) return false;
-                    if (!wait_bar(&p_full[gi & 1], (gi >> 1) & 1, abort_flag, p.status)) return false;
-                    tc_fence_after();
-                    const uint32_t tP = tmem + px_col_s(gi & 1);
-                    const uint64_t dV = dV0 + static_cast<uint64_t>(vb * (S::kVBytes >> 4));
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc_mma_bf16_ts(tO, tP + 8 * k, dV + static_cast<uint64_t>((k >> 2) * (S::kVHalf >> 4) + 2 * (k & 3)),
-                                       kPxIdPV, (i > 0 || k > 0) ? 1u : 0u);
-                    tc_commit(&pv_done[gi & 1]);
-                    tc_commit(&v_empty[vb]);
-                    return true;
-                };
-                ok = issue_qk(0);
-                if (ok && T > 1) ok = issue_qk(1);
-                for (int i = 0; i < T && ok; ++i) {
-                    ok = issue_pv(i);
-                    if (ok && i + 2 < T) ok = issue_qk(i + 2);
-                }
-                if (!ok) break;
-                tc_commit(&q_empty[qb]);
-                tc_commit(o_full);
-                g += T;
-                ++c;
-            }
-            // Every tcgen05 operation issued above has completed once `drain` does.
-            tc_commit(drain);
-        }
-        __syncwarp();
-        (void)wait_peers(drain, 0);
-    } else if (warp >= kPxExpandWarp) {
-        // -------------------------------------------------------------- V expansion
-        // E4M3 byte s eeee mmm -> bf16 s 0000eeee mmm0000, which is the value times 2^-120
-        // (subnormals too), then times 2^(X + 120): exact. A thread takes 16 tokens of a
-        // channel at a time; of each four the order becomes 0, 2, 1, 3, the order in
-        // which P's columns are written.
-        const int tid = threadIdx.x - 32 * kPxExpandWarp;
-        const int j = tid & 7;  // 16-token chunk of the channel row
-        int g = 0;
-        bool ok = true;
-        for (int un = blockIdx.x; un < p.units && ok; un += gridDim.x) {
-            const PxUnit u = px_unit(p, un);
-            for (int i = 0; i < u.T; ++i) {
-                const int gi = g + i, sv = gi % kPxVStages, vb = gi & 1;
-                ok = wait_bar(&raw_full[sv], (gi / kPxVStages) & 1, abort_flag, p.status);
-                ok = __all_sync(0xffffffffu, ok && wait_bar(&v_empty[vb], ((gi >> 1) & 1) ^ 1, abort_flag, p.status));
-                if (!ok) break;
-                const uint32_t raw = smem_u32(smem + S::kRaw + sv * S::kRawBytes) + j * 16;
-                const uint8_t *sfv = smem + S::kSfV + sv * 512 + (j >> 1);
-                const uint32_t out = smem_u32(smem + S::kV + vb * S::kVBytes) + (j >> 2) * S::kVHalf;
-                // Tokens past the prefix may hold anything: their codes become zero.
-                const int left = p.len - (u.t0 + i) * 128 - 16 * j;  // valid tokens from this chunk's first on
-#pragma unroll 4
-                for (int it = 0; it < 8; ++it) {
-                    const int c = it * 16 + (tid >> 3);
-                    const uint4 v4 = lds128(raw + c * 128);
-                    uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
-                    int e = sfv[(c & 31) * 16 + (c >> 5) * 4] + 120;  // exponent field of 2^(X + 120)
-                    if (left < 16) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int n = left - 4 * q;  // valid bytes of the word
-                            w[q] = n <= 0 ? 0u : n >= 4 ? w[q] : w[q] & ((1u << (8 * n)) - 1u);
-                        }
-                        if (left <= 0) e = 127;
-                    }
-                    const int e1 = imin(e, 254);
-                    const uint32_t f = static_cast<uint32_t>(e1) * 0x00800080u;
-                    uint32_t o[8];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        o[2 * q] = mul_bf16x2(((w[q] << 4) & 0x07F007F0u) | ((w[q] << 8) & 0x80008000u), f);
-                        o[2 * q + 1] = mul_bf16x2(((w[q] >> 4) & 0x07F007F0u) | (w[q] & 0x80008000u), f);
-                    }
-                    if (e > 254) {  // values past 2^16: the rest of the power in a second factor
-                        const uint32_t f2 = static_cast<uint32_t>(e - 254 + 127) * 0x00800080u;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) o[q] = mul_bf16x2(o[q], f2);
-                    }
-                    // 16-byte pieces 2 (j % 4) and + 1 of the row; odd and even halves of the
-                    // lanes write them in opposite order, so 8 lanes meet 8 different banks.
-                    const uint32_t dst = out + c * 128;
-                    const int q0 = 2 * (j & 3), sw = c & 7, flip = j >> 2;
-                    const uint32_t a0 = dst + (((q0 + flip) ^ sw) << 4), a1 = dst + (((q0 + 1 - flip) ^ sw) << 4);
-                    sts128(a0, flip ? o[4] : o[0], flip ? o[5] : o[1], flip ? o[6] : o[2], flip ? o[7] : o[3]);
-                    sts128(a1, flip ? o[0] : o[4], flip ? o[1] : o[5], flip ? o[2] : o[6], flip ? o[3] : o[7]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&v_full[vb]);
-                    mbar_arrive(&raw_empty[sv]);
-                }
-            }
-            g += u.T;
-        }
-    } else if (warp < 8) {
+    if (warp < kPxSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         // ------------------------------------------------------------------ softmax
         const int quarter = warp & 3, set = warp >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_base + px_col_s(set);
-        const uint32_t a_ref = smem_u32(smem + S::kRef) + row * 4;
-        uint64_t *ref = ref_bar + quarter * 2;
+        const uint32_t a_ref = smem_u32(smem + S::kRef) + row * 4;  // + set * 512
+        const uint32_t ref = S::kRefBar + 8 * kPxSets * quarter;  // + 8 * set
         const float sc = p.scale_log2;
-        int g = 0, c = 0;
+        int k = 0;        // subtiles of this set so far
+        int first = set;  // how far this set's next subtile lies in its unit
+        int gt = 0;       // tiles of the units so far
         bool ok = true;
-        for (int un = blockIdx.x; un < p.units && ok; un += gridDim.x) {
-            const PxUnit u = px_unit(p, un);
-            const int T = u.T;
-            float m = 0.f;  // m_O as of this warp's last tile
-            for (int i = (set - g) & 1; i < T; i += 2) {
-                const int gi = g + i, k = gi >> 1;
-                ok = __all_sync(0xffffffffu, wait_bar(&s_full[set], k & 1, abort_flag, p.status));
+        for (int c = 0; ok; ++c) {  // units
+            ok = __all_sync(0xffffffffu, unit_wait(c));
+            const PxUnit &u = *unit_at(c);
+            if (!ok || u.T == 0) break;
+            const int n = 2 * u.T;
+            const int late = p.nq - 1 - (u.row0 + row - px_div(u.row0 + row, p.nq, p.m_nq) * p.nq);  // own keys after this row's token
+            float m = -INFINITY;  // m_O as of this warp's last subtile; -inf: no key yet
+            int i = first;
+            for (; i < n; i += kPxSets, ++k) {
+                ok = wait_warp(S::kSFull + 8 * set, k & 1);
                 if (!ok) break;
-                // The reference as the last tile's owner left it (posted long ago as a rule).
-                float prev = 0.f;
-                if (gi > 0) {
-                    ok = __all_sync(0xffffffffu, wait_bar(&ref[(gi - 1) & 1], ((gi - 1) >> 1) & 1, abort_flag, p.status));
-                    if (!ok) break;
-                    prev = __uint_as_float(lds32(a_ref + ((gi - 1) & 1) * 512));
-                }
                 tc_fence_after();
-                const int jv = p.len - (u.t0 + i) * 128;  // keys of the tile, at least 1
-                // 32 scores of the row; keys past the prefix are -inf.
-                auto load_scores = [&](int q, uint32_t (&s)[32]) { tc_ld_32x32b_x32(tS + 32 * q, s); };
-                auto mask = [&](int q, uint32_t (&s)[32]) {
-                    if (jv < 32 * q + 32) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (32 * q + j >= jv) s[j] = 0xFF800000u;
-                    }
-                };
-                // The row max first, in a pass of its own: the scores are read from TMEM
-                // again for the exponentials rather than held (128 of the 128 registers).
-                float hm = -INFINITY;
-#pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    uint32_t s0[32], s1[32];
-                    load_scores(q, s0);
-                    load_scores(q + 1, s1);
-                    tc_wait_ld32(s0);
-                    tc_wait_ld32(s1);
-                    mask(q, s0);
-                    mask(q + 1, s1);
-                    hm = fmax3(hm, max32(s0), max32(s1));
-                }
-                hm *= sc;
-                int E = 0;
-                if (i == 0) {
-                    m = hm > -INFINITY ? hm : 0.f;
-                } else {
-                    m = prev;
-                    if (hm - m > kPxMove) {
-                        const float up = ceilf(fminf(hm - m, kPxMaxMove));
-                        E = static_cast<int>(up);
-                        m += up;
-                    }
-                }
-                sts32(a_ref + (gi & 1) * 512, __float_as_uint(m));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ref[gi & 1]);
-                if (i > 0 && __any_sync(0xffffffffu, E != 0)) {
-                    // O holds the tiles before this one: scale its rows before P V(gi).
-                    ok = __all_sync(0xffffffffu,
-                                    wait_bar(&pv_done[(gi - 1) & 1], ((gi - 1) >> 1) & 1, abort_flag, p.status));
-                    if (!ok) break;
-                    tc_fence_after();
-                    rescale_o_lane(tmem + lane_base + kPxColO, S::kVRows, E);
-                }
-                const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
+                const PxTile tile = *reinterpret_cast<const PxTile *>(smem + S::kTiles + 8 * ((gt + (i >> 1)) & (kPxTiles - 1)));
+                const int lo = tile.rows & 0xFF, hi = (tile.rows >> 8) & 0xFF;
+                const bool active = lo < quarter * 32 + 32 && hi > quarter * 32;  // a row of the warp sees it
                 uint32_t s[2][32];
-                load_scores(0, s[0]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t (&cur)[32] = s[q & 1];
-                    tc_wait_ld32(cur);
-                    if (q < 3) load_scores(q + 1, s[(q + 1) & 1]);
-                    mask(q, cur);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 a = ffma2(make_float2(__uint_as_float(cur[4 * e]), __uint_as_float(cur[4 * e + 1])),
-                                               sc2, nm2);
-                        const float2 b = ffma2(
-                            make_float2(__uint_as_float(cur[4 * e + 2]), __uint_as_float(cur[4 * e + 3])), sc2, nm2);
-                        const float p0 = exp2_approx(a.x), p1 = exp2_approx(a.y);
-                        const float p2 = exp2_approx(b.x), p3 = exp2_approx(b.y);
-                        w[2 * e] = cvt_bf16x2(p0, p2);
-                        w[2 * e + 1] = cvt_bf16x2(p1, p3);
-                    }
-                    // Columns [16 q, 16 q + 16) hold scores that have been read (q >= 1: 16 q + 16
-                    // <= 32 q).
-                    tc_st_32x32b_x16(tS + 16 * q, w);
+                if (active) {
+                    tc_ld_32x32b_x32(tS, s[0]);
+                    tc_ld_32x32b_x32(tS + 32, s[1]);
+                    tc_wait_ld32(s[0]);
+                    tc_wait_ld32(s[1]);
                 }
-                tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[set]);
+                if (lane == 0) px_arrive(sb + S::kSFree + 8 * set);  // the next S of this set, while P is computed
+                float hm = -INFINITY;
+                if (active) {
+                    // Keys j < jv of the subtile are seen; a row of another sequence sees none.
+                    int jv = tile.keys - 64 * (i & 1);
+                    if (p.causal && (tile.rows >> 16)) jv -= late;
+                    const bool mine = row >= lo && row < hi;
+                    if (__builtin_expect(__any_sync(0xffffffffu, mine && jv < 64), 0)) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (j >= jv) s[j >> 5][j & 31] = 0xFF800000u;
+                    }
+                    hm = sc * fmaxf(max32(s[0]), max32(s[1]));
+                    if (!mine) hm = -INFINITY;
+                }
+                // The reference, after the last subtile's owner.
+                int E = 0;
+                const int ps = set == 0 ? kPxSets - 1 : set - 1, pk = (set == 0 ? k - 1 : k) & 1;
+                if (i > 0) {
+                    ok = wait_warp(ref + 8 * ps, pk);
+                    if (!ok) break;
+                    m = __uint_as_float(lds32(a_ref));
+                }
+                if (i == 0 || (hm > m && (m == -INFINITY || hm - m > kPxMove))) {
+                    if (m > -INFINITY) {
+                        E = static_cast<int>(ceilf(fminf(hm - m, kPxMaxMove)));
+                        m += static_cast<float>(E);
+                    } else {
+                        m = hm;
+                    }
+                    sts32(a_ref, __float_as_uint(m));
+                }
+                __syncwarp();
+                if (lane == 0) px_arrive(sb + ref + 8 * set);
+                // This set's P is free once P V of its last subtile is done. A warp without rows
+                // waits as well: else it could arrive at p_full a second time before the set's
+                // other warps have once.
+                ok = wait_warp(S::kPvDone + 8 * set, (k & 1) ^ 1);
+                if (!ok) break;
+                if (i > 0 && __any_sync(0xffffffffu, E != 0)) {
+                    // O holds the subtiles before this one: scale its rows before P V. (The phase
+                    // before the awaited one is complete: P V of this set's last subtile came
+                    // after it.)
+                    ok = wait_warp(S::kPvDone + 8 * ps, pk);
+                    if (!ok) break;
+                    tc_fence_after();
+                    px_rescale(tmem + lane_base + kPxColO, E);
+                }
+                tc_fence_after();
+                if (!active) {
+                    const uint32_t zero[16] = {};
+                    tc_st_32x32b_x16(tmem + lane_base + px_col_p(set), zero);
+                    tc_st_32x32b_x16(tmem + lane_base + px_col_p(set) + 16, zero);
+                    tc_wait_st();
+                } else {
+                    // p = 2^(s - m); 0 for a row that sees nothing here (hm = -inf).
+                    const float nm = hm > -INFINITY ? -m : -INFINITY;
+                    const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 a = ffma2(
+                                make_float2(__uint_as_float(s[q][4 * e]), __uint_as_float(s[q][4 * e + 1])), sc2, nm2);
+                            const float2 b = ffma2(
+                                make_float2(__uint_as_float(s[q][4 * e + 2]), __uint_as_float(s[q][4 * e + 3])), sc2, nm2);
+                            w[2 * e] = cvt_bf16x2(exp2_approx(a.x), exp2_approx(a.y));
+                            w[2 * e + 1] = cvt_bf16x2(exp2_approx(b.x), exp2_approx(b.y));
+                        }
+                        tc_st_32x32b_x16(tmem + lane_base + px_col_p(set) + 16 * q, w);
+                    }
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) px_arrive(sb + S::kPFull + 8 * set);
             }
+            const bool owns_last = i == n + kPxSets - 1;  // this set had the unit's last subtile
+            first = i - n;
+            gt += u.T;
             if (!ok) break;
             // -------------------------------------------------------------- epilogue
-            ok = __all_sync(0xffffffffu, wait_bar(o_full, c & 1, abort_flag, p.status));
+            ok = wait_warp(S::kOFull, c & 1);
             if (!ok) break;
-            tc_fence_after();
-            const float l = __uint_as_float(tc_ld_32x32b_x1(tmem + lane_base + kPxColO + 128));
-            tc_wait_ld();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const int n = u.q0 + row;
-            int64_t bh;
-            int t;
-            const int64_t part = px_row(p, u.h, n, bh, t) * p.splits + u.split;
-            float4 *dst = reinterpret_cast<float4 *>(p.ws_o + part * 128 + 64 * set);
+            if (quarter * 32 < u.rows) {
+                tc_fence_after();
+                const float l = __uint_as_float(tc_ld_32x32b_x1(tmem + lane_base + kPxColO + 128));
+                tc_wait_ld();
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const int un = u.qt * p.Hkv + u.h;
+                const int64_t slot = un + static_cast<int>(blockIdx.x);
+                // [slot][32 chunks of 4 channels][128 rows][4]: a warp stores its 32 rows side by side.
+                float4 *dst = reinterpret_cast<float4 *>(p.part_o) + slot * (32 * 128) + row;
+                for (int q = set; q < 4; q += kPxSets) {  // 32 channels at a time
+                    uint32_t o[32];
+                    tc_ld_32x32b_x32(tmem + lane_base + kPxColO + 32 * q, o);
+                    tc_wait_ld32(o);
+                    if (row < u.rows) {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                uint32_t o[32];
-                tc_ld_32x32b_x32(tmem + lane_base + kPxColO + 64 * set + 32 * hh, o);
-                tc_wait_ld32(o);
-                if (n < p.rows) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        dst[8 * hh + q] = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                                                      __uint_as_float(o[4 * q + 2]) * inv,
-                                                      __uint_as_float(o[4 * q + 3]) * inv);
+                        for (int e = 0; e < 8; ++e)
+                            dst[(8 * q + e) * 128] =
+                                make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                            __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                    }
+                }
+                // The owner of the unit's last subtile has m_O of its end.
+                if (owns_last && row < u.rows) p.part_lse[slot * 128 + row] = l > 0.f ? log2f(l) + m : -INFINITY;
+                if (threadIdx.x == 0) {
+                    if (u.edge & 1) p.first[un] = static_cast<int>(blockIdx.x);
+                    if (u.edge & 2) p.last[un] = static_cast<int>(blockIdx.x);
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                px_arrive(sb + S::kOFree);
+                unit_done(c);
+            }
+        }
+        if (!ok && lane == 0) px_give_up(abort_flag, p.status);
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kPxFeedWarp) {
+        // --------------------------------------------------------------------- feeder
+        // Announces the units, two ahead, gathers each one's query rows (the warp) and loads
+        // its key tiles (lane 0). A unit's rows come before its keys, so they are there
+        // when the unit before ends; the first unit's first keys come before.
+        PxIter it;
+        it.begin(p, lane);
+        int announced = 0;
+        auto announce = [&]() -> bool {
+            const int e = announced & (kPxUnits - 1);
+            if (!wait_warp(S::kUnitEmpty + 8 * e, ((announced / kPxUnits) & 1) ^ 1)) return false;
+            PxUnit v{};
+            (void)it.next(p, lane, v);
+            if (lane == 0) {
+                *reinterpret_cast<PxUnit *>(smem + S::kUnits + 64 * e) = v;
+                px_arrive(sb + S::kUnitFull + 8 * e);
+            }
+            __syncwarp();
+            ++announced;
+            return true;
+        };
+        int k_issued = 0, v_issued = 0;  // tiles
+        // The tile that comes next: of the prefix (seq < 0) or of sequence seq, whose own keys
+        // are len.
+        int *lens = reinterpret_cast<int *>(smem + S::kLens);
+        int seq = -1, tile = 0, len = 0;
+        // To the piece's first tile, by the warp.
+        auto seek = [&](const PxUnit &u) {
+            const int b0 = px_seq_lo(p, u.qt), b1 = px_seq_hi(p, u.qt);
+            if (p.own)
+                for (int b = b0 + lane; b <= b1; b += 32) lens[b - b0] = px_own_len(p, b);
+            __syncwarp();
+            seq = -1;
+            tile = u.t0;
+            len = p.len;
+            for (int b = b0 - 1; tile >= (len + 127) >> 7 && b < b1;) {
+                tile -= (len + 127) >> 7;
+                seq = ++b;
+                len = lens[b - b0];
+            }
+        };
+        // `count` more tiles of unit u, by lane 0.
+        auto load = [&](const PxUnit &u, int count) -> bool {
+            const int b0 = px_seq_lo(p, u.qt);
+            int row = 0, blk = 0;
+            if (count > 0) px_tile(p, u.h, seq, tile, row, blk);
+            for (int i = 0; i < count; ++i) {
+                const bool own = seq >= 0;
+                // Rows of the row tile that see it.
+                const int lo = own ? imax(seq * p.gq - u.row0, 0) : 0;
+                const int hi = own ? imin((seq + 1) * p.gq - u.row0, 128) : 128;
+                const PxTile t{lo | (hi << 8) | (own ? 1 << 16 : 0), len - tile * 128};
+                const CUtensorMap *mk = own ? &tmap_k : &tmap_pk, *mv = own ? &tmap_v : &tmap_pv;
+                const int nblk = own ? p.own_blocks : p.prefix_blocks;
+                const int64_t at = (static_cast<int64_t>(row) * nblk + blk) * 512;
+                const uint8_t *ks = (own ? p.k_scales : p.p_k_scales) + at, *vs = (own ? p.v_scales : p.p_v_scales) + at;
+                const int kc = blk * 128, krow = row, vt = row * nblk + blk;
+                // The next one, looked up ahead of the waits.
+                if (i + 1 < count) {
+                    for (++tile; tile * 128 >= len; tile = 0) {
+                        seq = seq < 0 ? b0 : seq + 1;
+                        len = lens[seq - b0];
+                    }
+                    px_tile(p, u.h, seq, tile, row, blk);
+                }
+                const int gi = k_issued;
+                const int st = gi & (kPxKStages - 1), sv = gi & (kPxVStages - 1);
+                uint64_t *kf = reinterpret_cast<uint64_t *>(smem + S::kKFull + 8 * st);
+                uint64_t *rf = reinterpret_cast<uint64_t *>(smem + S::kRawFull + 8 * sv);
+                if (!wait(S::kKEmpty + 8 * st, ((gi / kPxKStages) & 1) ^ 1)) return false;
+                // (The tile eight before is done with: S of the one four before is in the tensor core's
+                // past, so every set has gone on from the eighth.)
+                *reinterpret_cast<PxTile *>(smem + S::kTiles + 8 * (gi & (kPxTiles - 1))) = t;
+                mbar_arrive_expect_tx(kf, S::kKBytes + 512);
+                tma_load_3d(smem + S::kK + st * S::kKBytes, mk, 0, kc, krow, kf);
+                bulk_load(smem + S::kSfK + st * 512, ks, 512, kf);
+                k_issued = gi + 1;
+                if (!wait(S::kRawEmpty + 8 * sv, ((gi / kPxVStages) & 1) ^ 1)) return false;
+                mbar_arrive_expect_tx(rf, S::kRawBytes + 512);
+                tma_load_3d(smem + S::kRaw + sv * S::kRawBytes, mv, 0, 0, vt, rf);
+                bulk_load(smem + S::kSfV + sv * 512, vs, 512, rf);
+                v_issued = gi + 1;
+            }
+            return true;
+        };
+        // One past the tile that was loaded last (in load, the last one stays current).
+        auto step = [&](const PxUnit &u) {
+            const int b0 = px_seq_lo(p, u.qt);
+            for (++tile; tile * 128 >= len; tile = 0) {
+                seq = seq < 0 ? b0 : seq + 1;
+                len = lens[seq - b0];
+            }
+        };
+        bool ok = announce() && announce();
+        for (int c = 0; ok; ++c) {
+            const PxUnit &u = *unit_at(c);
+            if (u.T == 0) break;
+            const int qb = c & 1;
+            seek(u);
+            int loaded = 0;
+            if (c == 0) {
+                loaded = imin(u.T, imin(kPxKStages, kPxVStages));
+                if (lane == 0) {
+                    ok = load(u, loaded);
+                    if (loaded < u.T) step(u);
                 }
             }
-            if (n < p.rows && ((g + T - 1) & 1) == set) p.ws_lse[part] = l > 0.f ? log2f(l) + m : -INFINITY;
-            tc_fence_before();
+            ok = __all_sync(0xffffffffu, ok) && announce() && wait_warp(S::kQEmpty + 8 * qb, ((c >> 1) & 1) ^ 1);
+            if (!ok) break;
+            uint8_t *qbuf = smem + S::kQ + qb * S::kQBytes;
+            uint8_t *sfq = smem + S::kSfQ + qb * 512;
+            // Copies that need no register, all in flight: this warp has few, and a spilled one
+            // goes to L2 (shared memory leaves next to no L1). Lane l finds rows l + 32 j and
+            // copies their scales; then 16-byte chunk l % 4 of rows l / 4 + 8 i. Rows past the
+            // unit's are zero.
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                const int r = lane + 32 * j;
+                int at = -1;  // the row of 64 bytes of codes
+                int64_t sf = 0;
+                if (r < u.rows) {
+                    int t;
+                    const int64_t bh = px_row(p, u.h, u.row0 + r, t);
+                    at = static_cast<int>(bh * p.q_cap) + t;
+                    sf = bh * (p.q_cap / 128) * 512 + t * 16;
+                }
+                px_copy4(smem_u32(sfq + lane * 16 + j * 4), p.q_scales + sf, at >= 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = 32 * j + (lane >> 2) + 8 * i;
+                    const int a = __shfl_sync(0xffffffffu, at, (lane >> 2) + 8 * i);
+                    px_copy16(smem_u32(qbuf + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4)),
+                              p.q_codes + static_cast<int64_t>(imax(a, 0)) * 64 + (lane & 3) * 16, a >= 0);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
-            g += T;
-            ++c;
+            if (lane == 0) {
+                if (!(p.test_stall && c == 0)) px_arrive(sb + S::kQFull + 8 * qb);
+                ok = load(u, u.T - loaded);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (lane == 0) {
+            if (!ok) px_give_up(abort_flag, p.status);
+            // Let every issued copy land before the CTA can retire.
+            auto settle = [&](uint32_t bar, uint32_t parity) {
+                const uint64_t t0 = globaltimer_ns();
+                while (!px_try(bar, parity))
+                    if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
+            };
+            for (int i = imax(0, k_issued - kPxKStages); i < k_issued; ++i)
+                settle(sb + S::kKFull + 8 * (i % kPxKStages), (i / kPxKStages) & 1);
+            for (int i = imax(0, v_issued - kPxVStages); i < v_issued; ++i)
+                settle(sb + S::kRawFull + 8 * (i % kPxVStages), (i / kPxVStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kPxQkWarp) {
+        // ------------------------------------------------------------- Q K^T issuer
+        // Each of the three products (S, P V, D) has an issuing thread of its own.
+        if (elect_one()) {
+            const uint32_t tSfQ = tmem + kPxColSfQ, tSfK = tmem + kPxColSfK;
+            int g = 0, set = 0;  // tiles, the next S buffer
+            uint32_t sph = 1;    // s_free's parity for it: free at first
+            bool ok = true;
+            for (int c = 0; ok; ++c) {
+                const int qb = c & 1;
+                ok = unit_wait(c);
+                const int T = unit_at(c)->T;
+                if (!ok || T == 0) break;
+                unit_done(c);
+                ok = wait(S::kQFull + 8 * qb, (c >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t dQ = px_desc_lo(sb + S::kQ + qb * S::kQBytes, 16);
+                px_cp_atom(tSfQ, px_desc_lo(sb + S::kSfQ + qb * 512, 0));
+                for (int i = 0; i < T; ++i, ++g) {
+                    const int st = g & (kPxKStages - 1);
+                    ok = wait(S::kKFull + 8 * st, (g / kPxKStages) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    px_cp_atom(tSfK, px_desc_lo(sb + S::kSfK, 0) + st * 32);
+                    const uint32_t dK = px_desc_lo(sb + S::kK, 16) + st * (S::kKBytes >> 4);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ok = wait(S::kSFree + 8 * set, sph);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t tS = tmem + px_col_s(set), dKh = dK + half * (64 * 64 / 16);
+                        px_mma_mxf4<px_sf_id(kPxIdQK, 0)>(tS, dQ, dKh, tSfQ, tSfK + 2 * half, 0u);
+                        px_mma_mxf4<px_sf_id(kPxIdQK, 2)>(tS, dQ + 2, dKh + 2, tSfQ | (2u << 30),
+                                                          (tSfK + 2 * half) | (2u << 30), 1u);
+                        px_commit(sb + S::kSFull + 8 * set);
+                        if (++set == kPxSets) {
+                            set = 0;
+                            sph ^= 1;
+                        }
+                    }
+                    if (!ok) break;
+                    px_commit(sb + S::kKEmpty + 8 * st);
+                }
+                if (!ok) break;
+                px_commit(sb + S::kQEmpty + 8 * qb);
+            }
+            if (!ok) px_give_up(abort_flag, p.status);
+            // Every tcgen05 operation of the issuers has completed once `drain` does.
+            px_commit(sb + S::kDrain);
+        }
+        __syncwarp();
+        (void)wait_peers(reinterpret_cast<uint64_t *>(smem + S::kDrain), 0);
+    } else if (warp == kPxPvWarp) {
+        // --------------------------------------------------------------- P V issuer
+        if (elect_one()) {
+            const uint32_t tO = tmem + kPxColO, dV0 = px_desc_lo(sb + S::kV, 16);
+            int k = 0, set = 0;  // subtiles, the next set
+            uint32_t pph = 0;
+            bool ok = true;
+            for (int c = 0; ok; ++c) {
+                ok = unit_wait(c);
+                const int n = 2 * unit_at(c)->T;
+                if (!ok || n == 0) break;
+                unit_done(c);
+                for (int i = 0; i < n; ++i, ++k) {
+                    const int slot = k & (kPxVSlots - 1);
+                    ok = wait(S::kVFull + 8 * slot, (k / kPxVSlots) & 1);
+                    if (ok && i == 0 && c >= 1) ok = wait(S::kOFree, (c - 1) & 1);
+                    ok = ok && wait(S::kPFull + 8 * set, pph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t dV = dV0 + slot * (S::kVHalf >> 4), tP = tmem + px_col_p(set);
+                    px_mma_bf16<true>(tO, tP, dV, i > 0 ? 1u : 0u);
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) px_mma_bf16<false>(tO, tP + 8 * q, dV + 2 * q, 1u);
+                    px_commit(sb + S::kPvDone + 8 * set);
+                    px_commit(sb + S::kVEmpty + 8 * slot);
+                    if (++set == kPxSets) {
+                        set = 0;
+                        pph ^= 1;
+                    }
+                }
+                if (!ok) break;
+                px_commit(sb + S::kOFull);
+            }
+            if (!ok) px_give_up(abort_flag, p.status);
+            px_commit(sb + S::kDrain);
+        }
+        __syncwarp();
+    } else if (warp == kPxDWarp) {
+        // ----------------------------------------------------------------- D issuer
+        // D = V of 64 tokens, a channel per TMEM lane and a token per column: the E4M3 codes
+        // times a unit matrix, which the tensor core expands with their scales.
+        const uint32_t tD = tmem + kPxColD, tSfV = tmem + kPxColSfV, tOne = tmem + kPxColOne;
+        const uint32_t dUnit = px_desc_lo(sb + S::kUnit, 16);
+        if (lane == 0) px_cp_atom(tOne, px_desc_lo(sb + S::kSfOne, 0));
+        int g = 0;
+        bool ok = true;
+        for (int c = 0; ok; ++c) {
+            ok = __all_sync(0xffffffffu, unit_wait(c));
+            const int T = unit_at(c)->T;
+            if (!ok || T == 0) break;
+            __syncwarp();
+            if (lane == 0) unit_done(c);
+            for (int i = 0; i < T; ++i, ++g) {
+                const int sv = g & (kPxVStages - 1);
+                ok = wait_warp(S::kRawFull + 8 * sv, (g / kPxVStages) & 1);
+                if (!ok) break;
+                const int jv = reinterpret_cast<const PxTile *>(smem + S::kTiles + 8 * (g & (kPxTiles - 1)))->keys;
+                if (__builtin_expect(jv < 128, 0)) {
+                    // Codes past the last token may be anything (a NaN would spread): zeros.
+                    for (int ch = lane; ch < 128; ch += 32) {
+                        uint8_t *row = smem + S::kRaw + sv * S::kRawBytes + ch * 128;
+                        for (int q = jv >> 4; q < 8; ++q) {
+                            uint8_t *chunk = row + ((q ^ (ch & 7)) << 4);
+                            if (16 * q >= jv)
+                                *reinterpret_cast<uint4 *>(chunk) = make_uint4(0, 0, 0, 0);
+                            else
+                                for (int e = jv - 16 * q; e < 16; ++e) chunk[e] = 0;
+                        }
+                        uint8_t *sfv = smem + S::kSfV + sv * 512 + (ch & 31) * 16 + (ch >> 5) * 4;
+                        for (int q = (jv + 31) >> 5; q < 4; ++q) sfv[q] = 0;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    tc_fence_after();
+                    px_cp_atom(tSfV, px_desc_lo(sb + S::kSfV, 0) + sv * 32);
+                    const uint32_t dRaw = px_desc_lo(sb + S::kRaw, 16) + sv * (S::kRawBytes >> 4);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        // The four warps have read the D before: subtile 2 g + half - 1.
+                        if ((g > 0 || half > 0) && !wait(S::kDFree, half ^ 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            px_mma_mxf8(tD + 32 * q, dRaw + 4 * half + 2 * q, dUnit, px_sf_id(kPxIdD, 2 * half + q),
+                                        tSfV | ((2u * half + q) << 30), tOne | ((2u * half + q) << 30));
+                        px_commit(sb + S::kDFull);
+                    }
+                    px_commit(sb + S::kRawEmpty + 8 * sv);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
+        }
+        if (!ok && lane == 0) px_give_up(abort_flag, p.status);
+        if (lane == 0) px_commit(sb + S::kDrain);
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------------- V expansion
+        // A thread takes its channel's 64 values of D to bf16 (exact: an E4M3 value times a
+        // power of two has 4 significant bits) and into the swizzled K-major row that P V
+        // reads: one conversion for two values. (By shifts and multiplies on the codes it
+        // took 9 instructions for four, as many as all of the softmax.)
+        const int quarter = warp & 3, ch = quarter * 32 + lane;
+        const uint32_t tD = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kPxColD;
+        int k = 0;
+        bool ok = true;
+        for (int c = 0; ok; ++c) {
+            ok = __all_sync(0xffffffffu, unit_wait(c));
+            const int n = 2 * unit_at(c)->T;
+            if (!ok || n == 0) break;
+            __syncwarp();
+            if (lane == 0) unit_done(c);
+            for (int i = 0; i < n; ++i, ++k) {
+                const int slot = k & (kPxVSlots - 1);
+                ok = wait_warp(S::kVEmpty + 8 * slot, ((k / kPxVSlots) & 1) ^ 1) && wait_warp(S::kDFull, k & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t row = sb + S::kV + slot * S::kVHalf + ch * 128;
+                uint32_t d[32];
+                tc_ld_32x32b_x32(tD, d);
+                tc_wait_ld32(d);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = cvt_bf16x2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
+                    if (q == 0) {
+                        tc_ld_32x32b_x32(tD + 32, d);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) px_arrive(sb + S::kDFree);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sts128(row + (((4 * q + e) ^ (ch & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    if (q == 0) tc_wait_ld32(d);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) px_arrive(sb + S::kVFull + 8 * slot);
+            }
+        }
+        if (!ok && lane == 0) px_give_up(abort_flag, p.status);
+    }
+    }
+    teardown_tmem(warp == kPxQkWarp, tmem, kPxTmemCols);
+}
+
+// Joins the partial results of each query row: those of its unit, one for each share the
+// unit has a part in, in slots unit + share. A CTA takes 32 rows and 32 channels of a unit,
+// a warp four channels, a lane a row, as they are stored; then through shared memory to
+// whole rows. Eight partials are in flight: a unit of few rows and a long prefix has tens.
+constexpr int kMergeBatch = 8;
+__global__ void __launch_bounds__(256) qk4v8_prefix_merge_kernel(const PrefixParams p, __nv_bfloat16 *__restrict__ out,
+                                                                 float *__restrict__ lse) {
+    __shared__ uint2 tile[32][9];  // [row][chunk], 4 bf16
+    const int un = static_cast<int>(blockIdx.x >> 4);
+    const int row0 = (blockIdx.x >> 2 & 3) * 32;  // of the unit
+    const int chunk0 = (blockIdx.x & 3) * 8;
+    const int qt = un / p.Hkv, h = un - qt * p.Hkv;
+    if (qt * 128 + row0 >= p.rows) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = row0 + lane;
+    const int n = qt * 128 + row;  // of the KV head
+    // (A row without a key may belong to a unit without a tile, which nobody wrote. The counts are
+    // held to the shares there are: a kernel that gave up leaves none.)
+    const bool in = n < p.rows;
+    const int c0 = imax(0, imin(p.first[un], p.shares - 1));
+    const int np = imax(0, imin(p.last[un], p.shares - 1) - c0 + 1);
+    const bool keys = in && (p.tiles > 0 || px_own_len(p, px_div(n, p.gq, p.m_gq)) > 0);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f, m = -INFINITY;
+    if (keys) {
+        const float *lp = p.part_lse + static_cast<int64_t>(un + c0) * 128 + row;
+        const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + static_cast<int64_t>(un + c0) * (32 * 128) +
+                           (chunk0 + warp) * 128 + row;
+        for (int s0 = 0; s0 < np; s0 += kMergeBatch) {
+            float l[kMergeBatch];
+            float4 v[kMergeBatch];
+#pragma unroll
+            for (int s = 0; s < kMergeBatch; ++s) {
+                l[s] = -INFINITY;
+                v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s0 + s < np) {
+                    l[s] = lp[(s0 + s) * 128];
+                    v[s] = po[static_cast<int64_t>(s0 + s) * (32 * 128)];
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int s = 0; s < kMergeBatch; ++s) top = fmaxf(top, l[s]);
+            if (top == -INFINITY) continue;
+            const float w0 = exp2f(m - top);
+            m = top;
+            sum *= w0;
+            acc.x *= w0, acc.y *= w0, acc.z *= w0, acc.w *= w0;
+#pragma unroll
+            for (int s = 0; s < kMergeBatch; ++s) {
+                const float w = exp2f(l[s] - m);
+                sum += w;
+                acc.x += w * v[s].x;
+                acc.y += w * v[s].y;
+                acc.z += w * v[s].z;
+                acc.w += w * v[s].w;
+            }
         }
     }
-    teardown_tmem(warp == kPxMmaWarp, tmem, kPxTmemCols);
-}
-
-// Joins the partial results of each query row: `splits` of the prefix and `own_splits` of
-// its own keys (either may be 0). One warp per row, four channels a lane.
-__global__ void __launch_bounds__(256) qk4v8_prefix_merge_kernel(const float *__restrict__ o, const float *__restrict__ l,
-                                                                 int splits, const float *__restrict__ own_o,
-                                                                 const float *__restrict__ own_l, int own_splits,
-                                                                 int64_t rows, int Hq, int nq,
-                                                                 __nv_bfloat16 *__restrict__ out,
-                                                                 float *__restrict__ lse) {
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (r >= rows) return;
-    const int lane = threadIdx.x & 31;
-    const float *lp = l + r * splits, *lo = own_l + r * own_splits;
-    float m = -INFINITY;
-    for (int s = lane; s < splits + own_splits; s += 32) m = fmaxf(m, s < splits ? lp[s] : lo[s - splits]);
-    m = warp_max_f32(m);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    if (m > -INFINITY) {
-        auto add = [&](const float *po, float ls) {
-            const float w = exp2f(ls - m);
-            const float4 v = *reinterpret_cast<const float4 *>(po + lane * 4);
-            sum += w;
-            acc.x += w * v.x;
-            acc.y += w * v.y;
-            acc.z += w * v.z;
-            acc.w += w * v.w;
-        };
-#pragma unroll 4
-        for (int s = 0; s < splits; ++s) add(o + (r * splits + s) * 128, lp[s]);
-#pragma unroll 4
-        for (int s = 0; s < own_splits; ++s) add(own_o + (r * own_splits + s) * 128, lo[s]);
-    }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int64_t bh = r / nq;
-    const int t = static_cast<int>(r - bh * nq);
-    const int64_t b = bh / Hq;
-    const int h = static_cast<int>(bh - b * Hq);
-    uint2 w;
-    w.x = cvt_bf16x2(acc.x * inv, acc.y * inv);
-    w.y = cvt_bf16x2(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2 *>(out + ((b * nq + t) * Hq + h) * 128 + lane * 4) = w;
-    if (lse && lane == 0) lse[r] = sum > 0.f ? (log2f(sum) + m) * 0.6931471805599453f : -INFINITY;
+    tile[lane][warp] = make_uint2(cvt_bf16x2(acc.x * inv, acc.y * inv), cvt_bf16x2(acc.z * inv, acc.w * inv));
+    int t;
+    if (lse && chunk0 + warp == 0 && in) {
+        const int64_t bh = px_row(p, h, n, t);
+        lse[bh * p.nq + t] = sum > 0.f ? (log2f(sum) + m) * 0.6931471805599453f : -INFINITY;
+    }
+    __syncthreads();
+    const int r = threadIdx.x >> 3, c = threadIdx.x & 7;
+    if (qt * 128 + row0 + r >= p.rows) return;
+    const int64_t bh = px_row(p, h, qt * 128 + row0 + r, t);
+    const int64_t b = bh / p.Hq;
+    reinterpret_cast<uint2 *>(out + ((b * p.nq + t) * p.Hq + (bh - b * p.Hq)) * 128)[chunk0 + c] = tile[r][c];
 }
 
-cudaError_t launch_prefix(const CUtensorMap &tk, const PrefixParams &p, cudaStream_t stream) {
+cudaError_t launch_prefix(const CUtensorMap &pk, const CUtensorMap &pv, const CUtensorMap &k, const CUtensorMap &v,
+                          const PrefixParams &p, void *out, float *lse, cudaStream_t stream) {
     constexpr int kMaxDevices = 64;
     static bool configured[kMaxDevices] = {};
-    static int sm_count[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int sms = dev < kMaxDevices ? sm_count[dev] : 0;
     if (dev >= kMaxDevices || !configured[dev]) {
         e = cudaFuncSetAttribute(qk4v8_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PxSmem::kBytes);
         if (e != cudaSuccess) return e;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        if (dev < kMaxDevices) {
-            sm_count[dev] = sms;
-            configured[dev] = true;
-        }
+        if (dev < kMaxDevices) configured[dev] = true;
     }
-    const int grid = p.units < sms ? p.units : sms;
-    qk4v8_prefix_kernel<<<grid, kPxThreads, PxSmem::kBytes, stream>>>(tk, p);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_prefix_merge(const float *o, const float *l, int splits, const float *own_o, const float *own_l,
-                                int own_splits, int B, int Hq, int nq, void *out, float *lse, cudaStream_t stream) {
-    const int64_t rows = static_cast<int64_t>(B) * Hq * nq;
-    const int64_t grid = (rows + 7) / 8;
-    if (grid >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
-    qk4v8_prefix_merge_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-        o, l, splits, own_o, own_l, own_splits, rows, Hq, nq, static_cast<__nv_bfloat16 *>(out), lse);
+    if (p.shares > 0) {
+        qk4v8_prefix_kernel<<<p.shares, kPxThreads, PxSmem::kBytes, stream>>>(pk, pv, k, v, p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    qk4v8_prefix_merge_kernel<<<16u * static_cast<unsigned>(p.row_tiles) * static_cast<unsigned>(p.Hkv), 256, 0, stream>>>(
+        p, static_cast<__nv_bfloat16 *>(out), lse);
     return cudaGetLastError();
 }
 

@@ -104,24 +104,36 @@ cudaError_t launch_kv_append(const void *k, const void *v, int B, int n_new, int
                              int num_pages, uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes,
                              uint8_t *v_scales, void *tail, bool rotate_k, int32_t *seqlens_out, int32_t *status,
                              cudaStream_t stream);
-// The prefix part of a shared-prefix decode (prefix.cu).
+// Shared-prefix decode (prefix.cu).
 struct PrefixParams {
     const uint8_t *q_codes, *q_scales;            // [B][Hq][q_cap]
-    const uint8_t *k_scales, *v_codes, *v_scales; // [rows][row_blocks] blocks of 128 tokens
-    const int32_t *table;                         // pages of the prefix's tiles; null: contiguous
-    int num_pages, row_blocks;
-    int Hq, Hkv, G, nq, q_cap;
-    int len, tiles;                               // tokens of the prefix, and 128-key tiles
+    int B, Hq, Hkv, G, nq, q_cap;
+    int gq;                                       // G * nq
+    uint32_t m_gq, m_nq;                          // ceil(2^32 / gq), ceil(2^32 / nq), for px_div
     int rows, row_tiles;                          // query rows of a KV head (B * G * nq), and 128-row tiles
-    int splits, units;                            // units = splits * Hkv * row_tiles
     float scale_log2;
-    float *ws_o, *ws_lse;                         // [B][Hq][nq][splits][128], [B][Hq][nq][splits]
+    int causal;
+    // The prefix: tokens and 128-key tiles (0: none); scales [rows][prefix_blocks] blocks of
+    // 128 tokens; pages of its tiles (null: contiguous, [1][Hkv]).
+    int len, tiles, prefix_blocks;
+    const uint8_t *p_k_scales, *p_v_scales;
+    const int32_t *prefix_table;
+    // The sequences' own keys (own = 0: none), contiguous [B][Hkv][own_cap] or paged.
+    int own, own_cap, own_blocks;
+    const uint8_t *k_scales, *v_scales;
+    const int32_t *block_table, *seqlens;
+    int max_pages, num_pages;
+    // Partial results of unit u = row_tile * Hkv + head in share c, slot u + c: O
+    // [slot][32 chunks of 4 channels][128 rows][4] and log2-sum-exp [slot][128]; the first and last share of each unit.
+    int shares;
+    float *part_o, *part_lse;
+    int32_t *first, *last;
     int32_t *status;
     int test_stall;
 };
-cudaError_t launch_prefix(const CUtensorMap &tmap_k, const PrefixParams &p, cudaStream_t stream);
-cudaError_t launch_prefix_merge(const float *o, const float *l, int splits, const float *own_o, const float *own_l,
-                                int own_splits, int B, int Hq, int nq, void *out, float *lse, cudaStream_t stream);
+// The kernel over the prefix and the own keys on p.shares CTAs (0: no keys at all), then the merge.
+cudaError_t launch_prefix(const CUtensorMap &pk, const CUtensorMap &pv, const CUtensorMap &k, const CUtensorMap &v,
+                          const PrefixParams &p, void *out, float *lse, cudaStream_t stream);
 // Rotary positions of a call, as the kernels take them (rope.cuh).
 struct RopeParams {
     const float *table;         // (cos, sin) [max_pos][rotary / 2][2]

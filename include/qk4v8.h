@@ -496,27 +496,24 @@ QK4V8_API int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, 
  *   p_k_*, p_v_*  packed MXFP4 K and MXFP8 V of the prefix, [1][Hkv][prefix_cap]
  *            (the quantize calls with B = 1); prefix_len >= 0
  *   k_*, v_* the sequences' own caches, seqlens_k int32 [B] their lengths, which may
- *            be 0; max_seqlen a host bound on them, 0 when all are empty
- *   prefix_splits  parts the prefix is cut into, at most its 128-key tiles (0:
- *            qk4v8_decode_prefix_default_splits); num_splits as for
- *            qk4v8_attention_decode
- *   workspace  qk4v8_decode_prefix_workspace_bytes(B, Hq, nq, prefix_splits,
- *            num_splits) bytes with the counts used, 16-byte aligned. Calls that may
- *            overlap on the GPU need one each.
+ *            be 0; max_seqlen a host bound on them (0: all are empty; a longer one is cut
+ *            to it)
+ *   workspace  qk4v8_decode_prefix_workspace_bytes of the same sizes, 16-byte aligned.
+ *            Calls that may overlap on the GPU need one each.
  *   out, lse, softmax_scale, dev_status and errors as for qk4v8_attention_decode. A
  *            row with no key at all outputs 0 with lse = -inf.
- * Needs (Hq / Hkv) * nq <= 128. Three launches: the prefix kernel, the split kernel
- * of qk4v8_attention_decode over the own keys, the merge.
+ * Needs (Hq / Hkv) * nq <= 128. Two launches: the attention kernel over the prefix and
+ * the own keys, and the merge of its partial results.
  *
  * qk4v8_attention_decode_prefix_paged: the same over a pool of pages (see
  * qk4v8_kv_append): prefix_table int32 [ceil(prefix_len / 128)] (device) lists the
  * prefix's pages, block_table and seqlens_k hold the own parts, which begin on a
- * page of their own. Up to 64 query rows per KV head. A page index outside the pool
- * reads page 0 and reports QK4V8_ERR_INVALID_ARG in *dev_status.
+ * page of their own. A page index outside the pool reads page 0 and reports
+ * QK4V8_ERR_INVALID_ARG in *dev_status.
+ *
+ * qk4v8_decode_prefix_workspace_bytes: 0 for sizes that the calls refuse.
  */
-QK4V8_API size_t qk4v8_decode_prefix_workspace_bytes(int B, int Hq, int nq, int prefix_splits, int num_splits);
-
-QK4V8_API int qk4v8_decode_prefix_default_splits(int B, int Hq, int Hkv, int nq, int prefix_len);
+QK4V8_API size_t qk4v8_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int nq, int prefix_len, int max_seqlen);
 
 QK4V8_API int qk4v8_attention_decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq, int nq,
                                             int q_cap, const uint8_t *p_k_codes, const uint8_t *p_k_scales,
@@ -524,9 +521,8 @@ QK4V8_API int qk4v8_attention_decode_prefix(const uint8_t *q_codes, const uint8_
                                             int prefix_cap, const uint8_t *k_codes, const uint8_t *k_scales,
                                             const uint8_t *v_codes, const uint8_t *v_scales, int Hkv, int kv_cap,
                                             const int32_t *seqlens_k, int max_seqlen, int causal_in_block,
-                                            float softmax_scale, int prefix_splits, int num_splits, void *workspace,
-                                            size_t workspace_bytes, void *out, float *lse, int32_t *dev_status,
-                                            void *stream);
+                                            float softmax_scale, void *workspace, size_t workspace_bytes, void *out,
+                                            float *lse, int32_t *dev_status, void *stream);
 
 QK4V8_API int qk4v8_attention_decode_prefix_paged(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq,
                                                   int nq, int q_cap, const uint8_t *k_codes, const uint8_t *k_scales,
@@ -534,9 +530,8 @@ QK4V8_API int qk4v8_attention_decode_prefix_paged(const uint8_t *q_codes, const 
                                                   int num_pages, const int32_t *prefix_table, int prefix_len,
                                                   const int32_t *block_table, int max_pages, const int32_t *seqlens_k,
                                                   int max_seqlen, int causal_in_block, float softmax_scale,
-                                                  int prefix_splits, int num_splits, void *workspace,
-                                                  size_t workspace_bytes, void *out, float *lse, int32_t *dev_status,
-                                                  void *stream);
+                                                  void *workspace, size_t workspace_bytes, void *out, float *lse,
+                                                  int32_t *dev_status, void *stream);
 
 /*
  * Decode step from bf16 queries (MpFA QK4V8 article, section 3.2: the query's
