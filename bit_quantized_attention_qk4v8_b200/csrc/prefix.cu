@@ -95,20 +95,19 @@ struct PxSmem {
     static constexpr int kSfK = kSfQ + 2 * 512;
     static constexpr int kSfV = kSfK + kPxKStages * 512;
     static constexpr int kSfOne = kSfV + kPxVStages * 512;
-    static constexpr int kRef = kSfOne + 512;                     // float [128]: m_O of each row
-    static constexpr int kBar = kRef + 128 * 4;
+    static constexpr int kRef = kSfOne + 512;                     // (m_O, subtile) of each row
+    static constexpr int kBar = kRef + 128 * 8;
     // Barriers (byte offsets).
     static constexpr int kKFull = kBar, kKEmpty = kKFull + 8 * kPxKStages;             // per stage
     static constexpr int kRawFull = kKEmpty + 8 * kPxKStages;                          // per stage
     static constexpr int kRawEmpty = kRawFull + 8 * kPxVStages;
-    static constexpr int kDFull = kRawEmpty + 8 * kPxVStages, kDFree = kDFull + 8;
-    static constexpr int kVFull = kDFree + 8, kVEmpty = kVFull + 8 * kPxVSlots;        // per slot
+    static constexpr int kDFull = kRawEmpty + 8 * kPxVStages, kDFree = kDFull + 16;  // per half
+    static constexpr int kVFull = kDFree + 16, kVEmpty = kVFull + 8 * kPxVSlots;        // per slot
     static constexpr int kQFull = kVEmpty + 8 * kPxVSlots, kQEmpty = kQFull + 16;      // per Q buffer
     static constexpr int kSFull = kQEmpty + 16, kSFree = kSFull + 8 * kPxSets;         // per set
     static constexpr int kPFull = kSFree + 8 * kPxSets, kPvDone = kPFull + 8 * kPxSets;
     static constexpr int kOFull = kPvDone + 8 * kPxSets, kOFree = kOFull + 8, kDrain = kOFree + 8;
-    static constexpr int kRefBar = kDrain + 8;                                         // [quarter][set]
-    static constexpr int kUnitFull = kRefBar + 8 * 4 * kPxSets, kUnitEmpty = kUnitFull + 8 * kPxUnits;
+    static constexpr int kUnitFull = kDrain + 8, kUnitEmpty = kUnitFull + 8 * kPxUnits;
     static constexpr int kBarEnd = kUnitEmpty + 8 * kPxUnits;
     static constexpr int kMisc = (kBarEnd + 15) / 16 * 16;  // TMEM address, abort flag
     static constexpr int kUnits = kMisc + 16;          // PxUnit [kPxUnits]
@@ -248,6 +247,38 @@ __device__ __forceinline__ bool px_wait(uint32_t bar, uint32_t parity, uint32_t 
         : "=r"(ok)
         : "r"(bar), "r"(parity), "r"(flag), "n"(kWaitTimeoutNs)
         : "memory");
+    return ok != 0;
+}
+
+// The reference of a row goes from a subtile's owner to the next one's as one 8-byte word with
+// the subtile's number. px_take: false past kWaitTimeoutNs or once the abort flag is up.
+__device__ __forceinline__ void px_pass(uint32_t at, int seqno, float m) {
+    asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(__float_as_uint(m)), "r"(seqno) : "memory");
+}
+__device__ __forceinline__ bool px_take(uint32_t at, int seqno, uint32_t flag, float &m) {
+    uint32_t ok, v;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t1;\n\t.reg .b32 f, n;\n\t"
+        "ld.volatile.shared.v2.b32 {%1, n}, [%2];\n\t"
+        "setp.eq.s32 p, n, %3;\n\t"
+        "@p bra PX_DONE;\n\t"
+        "mov.u64 t0, %%globaltimer;\n\t"
+        "PX_AGAIN:\n\t"
+        "ld.volatile.shared.v2.b32 {%1, n}, [%2];\n\t"
+        "setp.eq.s32 p, n, %3;\n\t"
+        "@p bra PX_DONE;\n\t"
+        "ld.volatile.shared.b32 f, [%4];\n\t"
+        "mov.u64 t1, %%globaltimer;\n\t"
+        "sub.u64 t1, t1, t0;\n\t"
+        "setp.gt.u64 q, t1, %5;\n\t"
+        "setp.ne.or.b32 q, f, 0, q;\n\t"
+        "@!q bra PX_AGAIN;\n\t"
+        "PX_DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok), "=r"(v)
+        : "r"(at), "r"(seqno), "r"(flag), "n"(kWaitTimeoutNs)
+        : "memory");
+    m = __uint_as_float(v);
     return ok != 0;
 }
 
@@ -464,8 +495,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         init(S::kKEmpty, kPxKStages, 1);
         init(S::kRawFull, kPxVStages, 1);
         init(S::kRawEmpty, kPxVStages, 1);
-        init(S::kDFull, 1, 1);
-        init(S::kDFree, 1, 4);
+        init(S::kDFull, 2, 1);
+        init(S::kDFree, 2, 4);
         init(S::kVFull, kPxVSlots, 4);
         init(S::kVEmpty, kPxVSlots, 1);
         init(S::kQFull, 2, 1);
@@ -477,7 +508,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         init(S::kOFull, 1, 1);
         init(S::kOFree, 1, kPxSoftmaxWarps);
         init(S::kDrain, 1, 3);
-        init(S::kRefBar, 4 * kPxSets, 1);
         init(S::kUnitFull, kPxUnits, 1);
         // The three issuers, the expanding and the softmax warps.
         init(S::kUnitEmpty, kPxUnits, 3 + 4 + kPxSoftmaxWarps);
@@ -495,6 +525,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         tmem_alloc(tmem_slot, kPxTmemCols);
         tmem_relinquish();
     }
+    if (threadIdx.x < 128) px_pass(smem_u32(smem + S::kRef) + threadIdx.x * 8, -1, 0.f);
     if (warp >= kPxExpandWarp) {
         // Constant rows of the V slots (row 128 = 1.0, rows 129..143 = 0), the unit matrix
         // (E4M3 1.0 is 0x38) and the scales of 2^0.
@@ -515,6 +546,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         fence_proxy_async_smem();
     }
+    PxIter it;
+    if (warp == kPxFeedWarp) it.begin(p, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -531,8 +564,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const int row = quarter * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_base + px_col_s(set);
-        const uint32_t a_ref = smem_u32(smem + S::kRef) + row * 4;  // + set * 512
-        const uint32_t ref = S::kRefBar + 8 * kPxSets * quarter;  // + 8 * set
+        const uint32_t a_ref = smem_u32(smem + S::kRef) + row * 8;
         const float sc = p.scale_log2;
         int k = 0;        // subtiles of this set so far
         int first = set;  // how far this set's next subtile lies in its unit
@@ -547,8 +579,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             float m = -INFINITY;  // m_O as of this warp's last subtile; -inf: no key yet
             int i = first;
             for (; i < n; i += kPxSets, ++k) {
-                ok = wait_warp(S::kSFull + 8 * set, k & 1);
-                if (!ok) break;
+                // (A wait that gave up lets the warp go on with whatever is there, to one vote at
+                // the subtile's end: a vote after each was a tenth of the loop.)
+                ok = wait(S::kSFull + 8 * set, k & 1);
                 tc_fence_after();
                 const PxTile tile = *reinterpret_cast<const PxTile *>(smem + S::kTiles + 8 * ((gt + (i >> 1)) & (kPxTiles - 1)));
                 const int lo = tile.rows & 0xFF, hi = (tile.rows >> 8) & 0xFF;
@@ -579,12 +612,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 }
                 // The reference, after the last subtile's owner.
                 int E = 0;
-                const int ps = set == 0 ? kPxSets - 1 : set - 1, pk = (set == 0 ? k - 1 : k) & 1;
-                if (i > 0) {
-                    ok = wait_warp(ref + 8 * ps, pk);
-                    if (!ok) break;
-                    m = __uint_as_float(lds32(a_ref));
-                }
+                const int ps = set == 0 ? kPxSets - 1 : set - 1;
+                const int seqno = 2 * gt + i;  // the subtile's number in the share
+                if (i > 0) ok &= px_take(a_ref, seqno - 1, flag, m);
                 if (i == 0 || (hm > m && (m == -INFINITY || hm - m > kPxMove))) {
                     if (m > -INFINITY) {
                         E = static_cast<int>(ceilf(fminf(hm - m, kPxMaxMove)));
@@ -592,21 +622,17 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     } else {
                         m = hm;
                     }
-                    sts32(a_ref, __float_as_uint(m));
                 }
-                __syncwarp();
-                if (lane == 0) px_arrive(sb + ref + 8 * set);
+                px_pass(a_ref, seqno, m);
                 // This set's P is free once P V of its last subtile is done. A warp without rows
                 // waits as well: else it could arrive at p_full a second time before the set's
                 // other warps have once.
-                ok = wait_warp(S::kPvDone + 8 * set, (k & 1) ^ 1);
-                if (!ok) break;
-                if (i > 0 && __any_sync(0xffffffffu, E != 0)) {
+                ok &= wait(S::kPvDone + 8 * set, (k & 1) ^ 1);
+                if (i > 0 && __builtin_expect(__any_sync(0xffffffffu, E != 0), 0)) {
                     // O holds the subtiles before this one: scale its rows before P V. (The phase
                     // before the awaited one is complete: P V of this set's last subtile came
                     // after it.)
-                    ok = wait_warp(S::kPvDone + 8 * ps, pk);
-                    if (!ok) break;
+                    ok &= wait(S::kPvDone + 8 * ps, (set == 0 ? k - 1 : k) & 1);
                     tc_fence_after();
                     px_rescale(tmem + lane_base + kPxColO, E);
                 }
@@ -637,7 +663,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     tc_wait_st();
                 }
                 tc_fence_before();
-                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 if (lane == 0) px_arrive(sb + S::kPFull + 8 * set);
             }
             const bool owns_last = i == n + kPxSets - 1;  // this set had the unit's last subtile
@@ -689,9 +716,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // --------------------------------------------------------------------- feeder
         // Announces the units, two ahead, gathers each one's query rows (the warp) and loads
         // its key tiles (lane 0). A unit's rows come before its keys, so they are there
-        // when the unit before ends; the first unit's first keys come before.
-        PxIter it;
-        it.begin(p, lane);
+        // when the unit before ends.
         int announced = 0;
         auto announce = [&]() -> bool {
             const int e = announced & (kPxUnits - 1);
@@ -783,16 +808,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             const PxUnit &u = *unit_at(c);
             if (u.T == 0) break;
             const int qb = c & 1;
-            seek(u);
-            int loaded = 0;
-            if (c == 0) {
-                loaded = imin(u.T, imin(kPxKStages, kPxVStages));
-                if (lane == 0) {
-                    ok = load(u, loaded);
-                    if (loaded < u.T) step(u);
-                }
-            }
-            ok = __all_sync(0xffffffffu, ok) && announce() && wait_warp(S::kQEmpty + 8 * qb, ((c >> 1) & 1) ^ 1);
+            ok = wait_warp(S::kQEmpty + 8 * qb, ((c >> 1) & 1) ^ 1);
             if (!ok) break;
             uint8_t *qbuf = smem + S::kQ + qb * S::kQBytes;
             uint8_t *sfq = smem + S::kSfQ + qb * 512;
@@ -803,24 +819,35 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
                 const int r = lane + 32 * j;
-                int at = -1;  // the row of 64 bytes of codes
+                int64_t at = -1;  // the row of 64 bytes of codes
                 int64_t sf = 0;
                 if (r < u.rows) {
                     int t;
                     const int64_t bh = px_row(p, u.h, u.row0 + r, t);
-                    at = static_cast<int>(bh * p.q_cap) + t;
+                    at = bh * p.q_cap + t;
                     sf = bh * (p.q_cap / 128) * 512 + t * 16;
                 }
                 px_copy4(smem_u32(sfq + lane * 16 + j * 4), p.q_scales + sf, at >= 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rr = 32 * j + (lane >> 2) + 8 * i;
-                    const int a = __shfl_sync(0xffffffffu, at, (lane >> 2) + 8 * i);
+                    const int64_t a = __shfl_sync(0xffffffffu, at, (lane >> 2) + 8 * i);
                     px_copy16(smem_u32(qbuf + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4)),
-                              p.q_codes + static_cast<int64_t>(imax(a, 0)) * 64 + (lane & 3) * 16, a >= 0);
+                              p.q_codes + (a > 0 ? a : 0) * 64 + (lane & 3) * 16, a >= 0);
                 }
             }
+            seek(u);
+            int loaded = 0;
+            if (c == 0) {  // on their way together with the queries
+                loaded = imin(u.T, imin(kPxKStages, kPxVStages));
+                if (lane == 0) {
+                    ok = load(u, loaded);
+                    if (loaded < u.T) step(u);
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok) && announce();
             asm volatile("cp.async.wait_all;" ::: "memory");
+            if (!ok) break;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -975,18 +1002,16 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     px_cp_atom(tSfV, px_desc_lo(sb + S::kSfV, 0) + sv * 32);
                     const uint32_t dRaw = px_desc_lo(sb + S::kRaw, 16) + sv * (S::kRawBytes >> 4);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        // The four warps have read the D before: subtile 2 g + half - 1.
-                        if ((g > 0 || half > 0) && !wait(S::kDFree, half ^ 1)) {
+                    for (int q = 0; q < 4; ++q) {  // 32 tokens, into the halves of D in turn
+                        // The four warps have read what the half held (its use before this one).
+                        if ((g > 0 || q > 1) && !wait(S::kDFree + 8 * (q & 1), (q >> 1) ^ 1)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            px_mma_mxf8(tD + 32 * q, dRaw + 4 * half + 2 * q, dUnit, px_sf_id(kPxIdD, 2 * half + q),
-                                        tSfV | ((2u * half + q) << 30), tOne | ((2u * half + q) << 30));
-                        px_commit(sb + S::kDFull);
+                        px_mma_mxf8(tD + 32 * (q & 1), dRaw + 2 * q, dUnit, px_sf_id(kPxIdD, q),
+                                    tSfV | (static_cast<uint32_t>(q) << 30), tOne | (static_cast<uint32_t>(q) << 30));
+                        px_commit(sb + S::kDFull + 8 * (q & 1));
                     }
                     px_commit(sb + S::kRawEmpty + 8 * sv);
                 }
@@ -1015,30 +1040,27 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             if (lane == 0) unit_done(c);
             for (int i = 0; i < n; ++i, ++k) {
                 const int slot = k & (kPxVSlots - 1);
-                ok = wait_warp(S::kVEmpty + 8 * slot, ((k / kPxVSlots) & 1) ^ 1) && wait_warp(S::kDFull, k & 1);
-                if (!ok) break;
-                tc_fence_after();
+                ok = wait(S::kVEmpty + 8 * slot, ((k / kPxVSlots) & 1) ^ 1);
                 const uint32_t row = sb + S::kV + slot * S::kVHalf + ch * 128;
-                uint32_t d[32];
-                tc_ld_32x32b_x32(tD, d);
-                tc_wait_ld32(d);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < 2; ++q) {  // while the tensor core expands the other half
+                    ok &= wait(S::kDFull + 8 * q, k & 1);
+                    tc_fence_after();
+                    uint32_t d[32];
+                    tc_ld_32x32b_x32(tD + 32 * q, d);
+                    tc_wait_ld32(d);
+                    tc_fence_before();
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) px_arrive(sb + S::kDFree + 8 * q);
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = cvt_bf16x2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
-                    if (q == 0) {
-                        tc_ld_32x32b_x32(tD + 32, d);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) px_arrive(sb + S::kDFree);
-                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         sts128(row + (((4 * q + e) ^ (ch & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-                    if (q == 0) tc_wait_ld32(d);
                 }
+                if (!ok) break;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) px_arrive(sb + S::kVFull + 8 * slot);
