@@ -113,7 +113,8 @@ struct PxSmem {
     static constexpr int kUnits = kMisc + 16;          // PxUnit [kPxUnits]
     static constexpr int kTiles = kUnits + 64 * kPxUnits;   // PxTile [kPxTiles]
     static constexpr int kLens = kTiles + 8 * kPxTiles;     // int [kPxSeqs]: the unit's sequences
-    static constexpr int kUsed = kLens + 4 * kPxSeqs;
+    static constexpr int kNext = (kLens + 4 * kPxSeqs + 15) / 16 * 16;  // int4 [32]: the next tiles to load
+    static constexpr int kUsed = kNext + 16 * 32;
     static constexpr int kBytes = kUsed + 1024;
 };
 static_assert(PxSmem::kK % 1024 == 0 && PxSmem::kV % 1024 == 0 && PxSmem::kVHalf % 1024 == 0 &&
@@ -352,63 +353,72 @@ struct PxIter {
     __device__ __forceinline__ static int count(const PrefixParams &p, int qt, int lane) {
         int n = 0;
         if (p.own) {
+#pragma unroll 1
             for (int b = px_seq_lo(p, qt) + lane; b <= px_seq_hi(p, qt); b += 32) n += (px_own_len(p, b) + 127) >> 7;
             n = __reduce_add_sync(0xffffffffu, n);
         }
         return p.tiles + n;
     }
     __device__ __forceinline__ void begin(const PrefixParams &p, int lane) {
-        // The cost of row tile qt's units: a lane each (loads in flight together), or, of a few
-        // row tiles, by the warp.
-        auto cost = [&](int qt) -> int64_t {
-            if (qt >= p.row_tiles) return 0;
-            int n = p.tiles;
-            if (p.own) {
-                const int b1 = px_seq_hi(p, qt);
-#pragma unroll 8
-                for (int b = px_seq_lo(p, qt); b <= b1; ++b) n += (px_own_len(p, b) + 127) >> 7;
+        // The lanes share the row tiles: L lanes to one, which add up its sequences' tiles with
+        // their loads in flight together. Pass 0 finds the whole cost, pass 1 the row tile that
+        // holds this share's first tile. (All of it fits 31 bits: the host has seen to it.)
+        int log_l = 5;
+        while (log_l > 0 && (p.row_tiles << log_l) > 32) --log_l;
+        const int L = 1 << log_l, step = 32 >> log_l;
+        int w = 0, r = 0, c = 0;
+        left = qt = h = off = tiles = 0;
+#pragma unroll 1
+        for (int q0 = 0, pass = 0; pass < 2;) {
+            if (pass == 0 || p.row_tiles > step) {  // else c is still there
+                const int q = q0 + (lane >> log_l);
+                c = 0;
+                if (q < p.row_tiles && p.own) {
+                    const int b1 = px_seq_hi(p, q);
+#pragma unroll 4
+                    for (int b = px_seq_lo(p, q) + (lane & (L - 1)); b <= b1; b += L) c += (px_own_len(p, b) + 127) >> 7;
+                }
+#pragma unroll 1
+                for (int o = 1; o < L; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+                c = q < p.row_tiles && (lane & (L - 1)) == 0 ? px_span(p.tiles + c) * p.Hkv : 0;
             }
-            return static_cast<int64_t>(px_span(n)) * p.Hkv;
-        };
-        const bool few = p.row_tiles <= 8;
-        int64_t mine = 0, kept = 0;  // kept: lane i's, of row tile i
-        if (few) {
-            for (int q = 0; q < p.row_tiles; ++q) {
-                const int64_t v = static_cast<int64_t>(px_span(count(p, q, lane))) * p.Hkv;
-                if (lane == q) kept = mine = v;
+            if (pass == 0) {
+                w += __reduce_add_sync(0xffffffffu, c);
+            } else {
+                int sum = c;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += v;
+                }
+                const int k = __popc(__ballot_sync(0xffffffffu, sum <= r));  // lane k's row tile holds r
+                const int before = __shfl_sync(0xffffffffu, sum, k > 0 ? k - 1 : 0);
+                if (k > 0) r -= before;
+                if (k < 32) {
+                    qt = q0 + (k >> log_l);
+                    break;
+                }
             }
-        } else {
-            for (int q = lane; q < p.row_tiles; q += 32) mine += cost(q);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        const int64_t w = mine;
-        const int64_t share = (w + gridDim.x - 1) / gridDim.x;
-        int64_t r = blockIdx.x * share;
-        left = r < w ? static_cast<int>(share < w - r ? share : w - r) : 0;
-        qt = h = off = tiles = 0;
-        if (left == 0) return;
-        for (int q0 = 0;; q0 += 32) {  // ends: r < w
-            int64_t c = few ? kept : cost(q0 + lane);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, c, o);
-                if (lane >= o) c += v;
-            }
-            const int k = __popc(__ballot_sync(0xffffffffu, c <= r));  // row tile q0 + k holds r
-            const int64_t before = __shfl_sync(0xffffffffu, c, k > 0 ? k - 1 : 0);
-            if (k > 0) r -= before;
-            if (k < 32 || q0 + 32 >= p.row_tiles) {
-                qt = q0 + (k < 32 ? k : 31);
-                break;
+            q0 += step;
+            if (q0 >= p.row_tiles) {
+                if (pass == 0) {
+                    const int n = static_cast<int>(gridDim.x);
+                    const int share = (w + n - 1) / n;
+                    r = static_cast<int>(blockIdx.x) * share;
+                    if (r >= w) return;
+                    left = imin(share, w - r);
+                }
+                q0 = 0;
+                ++pass;
             }
         }
         tiles = count(p, qt, lane);
         const int span = imax(1, px_span(tiles));
-        h = static_cast<int>(r / span);
-        off = static_cast<int>(r - static_cast<int64_t>(h) * span);
+        h = r / span;
+        off = r - h * span;
     }
     __device__ __forceinline__ bool next(const PrefixParams &p, int lane, PxUnit &u) {
+#pragma unroll 1
         while (left > 0 && qt < p.row_tiles) {
             const int span = px_span(tiles);
             const int take = imin(left, span - off);
@@ -450,6 +460,11 @@ __device__ __forceinline__ void px_copy4(uint32_t dst, const void *src, bool any
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(any ? 4 : 0) : "memory");
 }
 
+// Arrives at the barrier once the thread's copies have landed.
+__device__ __forceinline__ void px_arrive_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Key tile `tile` of the prefix (seq < 0) or of a sequence's own keys: row and block of the
 // K/V arrays. A page outside the pool reads page 0 and is reported.
 __device__ __forceinline__ void px_tile(const PrefixParams &p, int h, int seq, int tile, int &row, int &blk) {
@@ -489,6 +504,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 
     if (threadIdx.x == 32) {
         auto init = [&](int offset, int n, uint32_t count) {
+#pragma unroll 1
             for (int i = 0; i < n; ++i) mbar_init(reinterpret_cast<uint64_t *>(smem + offset + 8 * i), count);
         };
         init(S::kKFull, kPxKStages, 1);
@@ -499,7 +515,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         init(S::kDFree, 2, 4);
         init(S::kVFull, kPxVSlots, 4);
         init(S::kVEmpty, kPxVSlots, 1);
-        init(S::kQFull, 2, 1);
+        init(S::kQFull, 2, 32);
         init(S::kQEmpty, 2, 1);
         init(S::kSFull, kPxSets, 1);
         init(S::kSFree, kPxSets, 4);
@@ -530,12 +546,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // Constant rows of the V slots (row 128 = 1.0, rows 129..143 = 0), the unit matrix
         // (E4M3 1.0 is 0x38) and the scales of 2^0.
         const int tid = threadIdx.x - 32 * kPxExpandWarp;
+#pragma unroll 1
         for (int i = tid; i < kPxVSlots * 16 * 8; i += 128) {
             const int slot = i >> 7, r = (i >> 3) & 15;
             const uint32_t v = r == 0 ? 0x3F803F80u : 0u;
             *reinterpret_cast<uint4 *>(smem + S::kV + slot * S::kVHalf + (128 + r) * 128 + (i & 7) * 16) =
                 make_uint4(v, v, v, v);
         }
+#pragma unroll 1
         for (int i = tid; i < 32 * 8; i += 128) {
             const int r = i >> 3, at = (i & 7) ^ (r & 7);  // row r's 16-byte chunk `at`
             uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -570,6 +588,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         int first = set;  // how far this set's next subtile lies in its unit
         int gt = 0;       // tiles of the units so far
         bool ok = true;
+#pragma unroll 1
         for (int c = 0; ok; ++c) {  // units
             ok = __all_sync(0xffffffffu, unit_wait(c));
             const PxUnit &u = *unit_at(c);
@@ -578,6 +597,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             const int late = p.nq - 1 - (u.row0 + row - px_div(u.row0 + row, p.nq, p.m_nq) * p.nq);  // own keys after this row's token
             float m = -INFINITY;  // m_O as of this warp's last subtile; -inf: no key yet
             int i = first;
+#pragma unroll 1
             for (; i < n; i += kPxSets, ++k) {
                 // (A wait that gave up lets the warp go on with whatever is there, to one vote at
                 // the subtile's end: a vote after each was a tenth of the loop.)
@@ -683,6 +703,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 const int64_t slot = un + static_cast<int>(blockIdx.x);
                 // [slot][32 chunks of 4 channels][128 rows][4]: a warp stores its 32 rows side by side.
                 float4 *dst = reinterpret_cast<float4 *>(p.part_o) + slot * (32 * 128) + row;
+#pragma unroll 1
                 for (int q = set; q < 4; q += kPxSets) {  // 32 channels at a time
                     uint32_t o[32];
                     tc_ld_32x32b_x32(tmem + lane_base + kPxColO + 32 * q, o);
@@ -715,8 +736,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     if (warp == kPxFeedWarp) {
         // --------------------------------------------------------------------- feeder
         // Announces the units, two ahead, gathers each one's query rows (the warp) and loads
-        // its key tiles (lane 0). A unit's rows come before its keys, so they are there
-        // when the unit before ends.
+        // its key tiles. A unit's rows come before its keys, so they are there when the unit
+        // before ends.
         int announced = 0;
         auto announce = [&]() -> bool {
             const int e = announced & (kPxUnits - 1);
@@ -736,77 +757,93 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // are len.
         int *lens = reinterpret_cast<int *>(smem + S::kLens);
         int seq = -1, tile = 0, len = 0;
+        // `ahead` tiles on, in a unit with rows of the sequences b0 .. b1.
+        auto walk = [&](int b0, int b1, int ahead) {
+#pragma unroll 1
+            for (;;) {
+                const int left = ((len + 127) >> 7) - tile;  // of the sequence's tiles
+                if (ahead < left || !p.own || seq == b1) break;
+                ahead -= left;
+                seq = seq < 0 ? b0 : seq + 1;
+                len = lens[seq - b0];
+                tile = 0;
+            }
+            tile += ahead;
+        };
         // To the piece's first tile, by the warp.
         auto seek = [&](const PxUnit &u) {
             const int b0 = px_seq_lo(p, u.qt), b1 = px_seq_hi(p, u.qt);
             if (p.own)
+#pragma unroll 1
                 for (int b = b0 + lane; b <= b1; b += 32) lens[b - b0] = px_own_len(p, b);
             __syncwarp();
             seq = -1;
-            tile = u.t0;
+            tile = 0;
             len = p.len;
-            for (int b = b0 - 1; tile >= (len + 127) >> 7 && b < b1;) {
-                tile -= (len + 127) >> 7;
-                seq = ++b;
-                len = lens[b - b0];
-            }
+            walk(b0, b1, u.t0);
         };
-        // `count` more tiles of unit u, by lane 0.
+        // `count` more tiles of unit u. The lanes look 32 tiles up at once (a page's number
+        // takes a trip to memory, and one after the other those took longer than the tiles),
+        // lane 0 loads them.
+        int4 *next = reinterpret_cast<int4 *>(smem + S::kNext);
         auto load = [&](const PxUnit &u, int count) -> bool {
-            const int b0 = px_seq_lo(p, u.qt);
-            int row = 0, blk = 0;
-            if (count > 0) px_tile(p, u.h, seq, tile, row, blk);
-            for (int i = 0; i < count; ++i) {
-                const bool own = seq >= 0;
-                // Rows of the row tile that see it.
-                const int lo = own ? imax(seq * p.gq - u.row0, 0) : 0;
-                const int hi = own ? imin((seq + 1) * p.gq - u.row0, 128) : 128;
-                const PxTile t{lo | (hi << 8) | (own ? 1 << 16 : 0), len - tile * 128};
-                const CUtensorMap *mk = own ? &tmap_k : &tmap_pk, *mv = own ? &tmap_v : &tmap_pv;
-                const int nblk = own ? p.own_blocks : p.prefix_blocks;
-                const int64_t at = (static_cast<int64_t>(row) * nblk + blk) * 512;
-                const uint8_t *ks = (own ? p.k_scales : p.p_k_scales) + at, *vs = (own ? p.v_scales : p.p_v_scales) + at;
-                const int kc = blk * 128, krow = row, vt = row * nblk + blk;
-                // The next one, looked up ahead of the waits.
-                if (i + 1 < count) {
-                    for (++tile; tile * 128 >= len; tile = 0) {
-                        seq = seq < 0 ? b0 : seq + 1;
-                        len = lens[seq - b0];
+            const int b0 = px_seq_lo(p, u.qt), b1 = px_seq_hi(p, u.qt);
+            bool ok = true;
+#pragma unroll 1
+            for (int i0 = 0; i0 < count && ok; i0 += 32) {
+                const int n = imin(32, count - i0);
+                // Lane l goes l tiles ahead; all start the next 32 from n ahead.
+                const int mine = imin(lane, n - 1);
+                walk(b0, b1, mine);
+                int row, blk;
+                px_tile(p, u.h, seq, tile, row, blk);
+                next[mine] = make_int4(seq, row, blk, len - tile * 128);
+                walk(b0, b1, n - mine);
+                __syncwarp();
+                if (lane == 0) {
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i) {
+                        const int4 d = next[i];
+                        const bool own = d.x >= 0;
+                        // Rows of the row tile that see it.
+                        const int lo = own ? imax(d.x * p.gq - u.row0, 0) : 0;
+                        const int hi = own ? imin((d.x + 1) * p.gq - u.row0, 128) : 128;
+                        const PxTile t{lo | (hi << 8) | (own ? 1 << 16 : 0), d.w};
+                        const CUtensorMap *mk = own ? &tmap_k : &tmap_pk, *mv = own ? &tmap_v : &tmap_pv;
+                        const int vt = d.y * (own ? p.own_blocks : p.prefix_blocks) + d.z;
+                        const int64_t at = static_cast<int64_t>(vt) * 512;
+                        const int gi = k_issued;
+                        const int st = gi & (kPxKStages - 1), sv = gi & (kPxVStages - 1);
+                        uint64_t *kf = reinterpret_cast<uint64_t *>(smem + S::kKFull + 8 * st);
+                        uint64_t *rf = reinterpret_cast<uint64_t *>(smem + S::kRawFull + 8 * sv);
+                        ok = wait(S::kKEmpty + 8 * st, ((gi / kPxKStages) & 1) ^ 1);
+                        if (!ok) break;
+                        // (The tile eight before is done with: S of the one four before is in the
+                        // tensor core's past, so every set has gone on from the eighth.)
+                        *reinterpret_cast<PxTile *>(smem + S::kTiles + 8 * (gi & (kPxTiles - 1))) = t;
+                        mbar_arrive_expect_tx(kf, S::kKBytes + 512);
+                        tma_load_3d(smem + S::kK + st * S::kKBytes, mk, 0, d.z * 128, d.y, kf);
+                        bulk_load(smem + S::kSfK + st * 512, (own ? p.k_scales : p.p_k_scales) + at, 512, kf);
+                        k_issued = gi + 1;
+                        ok = wait(S::kRawEmpty + 8 * sv, ((gi / kPxVStages) & 1) ^ 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(rf, S::kRawBytes + 512);
+                        tma_load_3d(smem + S::kRaw + sv * S::kRawBytes, mv, 0, 0, vt, rf);
+                        bulk_load(smem + S::kSfV + sv * 512, (own ? p.v_scales : p.p_v_scales) + at, 512, rf);
+                        v_issued = gi + 1;
                     }
-                    px_tile(p, u.h, seq, tile, row, blk);
                 }
-                const int gi = k_issued;
-                const int st = gi & (kPxKStages - 1), sv = gi & (kPxVStages - 1);
-                uint64_t *kf = reinterpret_cast<uint64_t *>(smem + S::kKFull + 8 * st);
-                uint64_t *rf = reinterpret_cast<uint64_t *>(smem + S::kRawFull + 8 * sv);
-                if (!wait(S::kKEmpty + 8 * st, ((gi / kPxKStages) & 1) ^ 1)) return false;
-                // (The tile eight before is done with: S of the one four before is in the tensor core's
-                // past, so every set has gone on from the eighth.)
-                *reinterpret_cast<PxTile *>(smem + S::kTiles + 8 * (gi & (kPxTiles - 1))) = t;
-                mbar_arrive_expect_tx(kf, S::kKBytes + 512);
-                tma_load_3d(smem + S::kK + st * S::kKBytes, mk, 0, kc, krow, kf);
-                bulk_load(smem + S::kSfK + st * 512, ks, 512, kf);
-                k_issued = gi + 1;
-                if (!wait(S::kRawEmpty + 8 * sv, ((gi / kPxVStages) & 1) ^ 1)) return false;
-                mbar_arrive_expect_tx(rf, S::kRawBytes + 512);
-                tma_load_3d(smem + S::kRaw + sv * S::kRawBytes, mv, 0, 0, vt, rf);
-                bulk_load(smem + S::kSfV + sv * 512, vs, 512, rf);
-                v_issued = gi + 1;
+                ok = __all_sync(0xffffffffu, ok);
             }
-            return true;
+            return ok;
         };
-        // One past the tile that was loaded last (in load, the last one stays current).
-        auto step = [&](const PxUnit &u) {
-            const int b0 = px_seq_lo(p, u.qt);
-            for (++tile; tile * 128 >= len; tile = 0) {
-                seq = seq < 0 ? b0 : seq + 1;
-                len = lens[seq - b0];
-            }
-        };
-        bool ok = announce() && announce();
+        bool ok = true;
+#pragma unroll 1
         for (int c = 0; ok; ++c) {
+#pragma unroll 1
+            while (ok && announced < c + 2) ok = announce();
             const PxUnit &u = *unit_at(c);
-            if (u.T == 0) break;
+            if (!ok || u.T == 0) break;
             const int qb = c & 1;
             ok = wait_warp(S::kQEmpty + 8 * qb, ((c >> 1) & 1) ^ 1);
             if (!ok) break;
@@ -828,7 +865,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     sf = bh * (p.q_cap / 128) * 512 + t * 16;
                 }
                 px_copy4(smem_u32(sfq + lane * 16 + j * 4), p.q_scales + sf, at >= 0);
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     const int rr = 32 * j + (lane >> 2) + 8 * i;
                     const int64_t a = __shfl_sync(0xffffffffu, at, (lane >> 2) + 8 * i);
@@ -836,36 +873,25 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                               p.q_codes + (a > 0 ? a : 0) * 64 + (lane & 3) * 16, a >= 0);
                 }
             }
+            // q_full completes with the copies; its waiter makes them visible to the tensor core.
+            if (!(p.test_stall && c == 0)) px_arrive_copies(sb + S::kQFull + 8 * qb);
             seek(u);
-            int loaded = 0;
-            if (c == 0) {  // on their way together with the queries
-                loaded = imin(u.T, imin(kPxKStages, kPxVStages));
-                if (lane == 0) {
-                    ok = load(u, loaded);
-                    if (loaded < u.T) step(u);
-                }
-            }
-            ok = __all_sync(0xffffffffu, ok) && announce();
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            if (!ok) break;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (!(p.test_stall && c == 0)) px_arrive(sb + S::kQFull + 8 * qb);
-                ok = load(u, u.T - loaded);
-            }
-            ok = __all_sync(0xffffffffu, ok);
+            ok = load(u, u.T);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (lane == 0) {
             if (!ok) px_give_up(abort_flag, p.status);
             // Let every issued copy land before the CTA can retire.
             auto settle = [&](uint32_t bar, uint32_t parity) {
                 const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
                 while (!px_try(bar, parity))
                     if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
             };
+#pragma unroll 1
             for (int i = imax(0, k_issued - kPxKStages); i < k_issued; ++i)
                 settle(sb + S::kKFull + 8 * (i % kPxKStages), (i / kPxKStages) & 1);
+#pragma unroll 1
             for (int i = imax(0, v_issued - kPxVStages); i < v_issued; ++i)
                 settle(sb + S::kRawFull + 8 * (i % kPxVStages), (i / kPxVStages) & 1);
         }
@@ -878,6 +904,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             int g = 0, set = 0;  // tiles, the next S buffer
             uint32_t sph = 1;    // s_free's parity for it: free at first
             bool ok = true;
+#pragma unroll 1
             for (int c = 0; ok; ++c) {
                 const int qb = c & 1;
                 ok = unit_wait(c);
@@ -886,9 +913,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 unit_done(c);
                 ok = wait(S::kQFull + 8 * qb, (c >> 1) & 1);
                 if (!ok) break;
+                fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t dQ = px_desc_lo(sb + S::kQ + qb * S::kQBytes, 16);
                 px_cp_atom(tSfQ, px_desc_lo(sb + S::kSfQ + qb * 512, 0));
+#pragma unroll 1
                 for (int i = 0; i < T; ++i, ++g) {
                     const int st = g & (kPxKStages - 1);
                     ok = wait(S::kKFull + 8 * st, (g / kPxKStages) & 1);
@@ -930,11 +959,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             int k = 0, set = 0;  // subtiles, the next set
             uint32_t pph = 0;
             bool ok = true;
+#pragma unroll 1
             for (int c = 0; ok; ++c) {
                 ok = unit_wait(c);
                 const int n = 2 * unit_at(c)->T;
                 if (!ok || n == 0) break;
                 unit_done(c);
+#pragma unroll 1
                 for (int i = 0; i < n; ++i, ++k) {
                     const int slot = k & (kPxVSlots - 1);
                     ok = wait(S::kVFull + 8 * slot, (k / kPxVSlots) & 1);
@@ -969,12 +1000,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (lane == 0) px_cp_atom(tOne, px_desc_lo(sb + S::kSfOne, 0));
         int g = 0;
         bool ok = true;
+#pragma unroll 1
         for (int c = 0; ok; ++c) {
             ok = __all_sync(0xffffffffu, unit_wait(c));
             const int T = unit_at(c)->T;
             if (!ok || T == 0) break;
             __syncwarp();
             if (lane == 0) unit_done(c);
+#pragma unroll 1
             for (int i = 0; i < T; ++i, ++g) {
                 const int sv = g & (kPxVStages - 1);
                 ok = wait_warp(S::kRawFull + 8 * sv, (g / kPxVStages) & 1);
@@ -982,16 +1015,20 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 const int jv = reinterpret_cast<const PxTile *>(smem + S::kTiles + 8 * (g & (kPxTiles - 1)))->keys;
                 if (__builtin_expect(jv < 128, 0)) {
                     // Codes past the last token may be anything (a NaN would spread): zeros.
+#pragma unroll 1
                     for (int ch = lane; ch < 128; ch += 32) {
                         uint8_t *row = smem + S::kRaw + sv * S::kRawBytes + ch * 128;
+#pragma unroll 1
                         for (int q = jv >> 4; q < 8; ++q) {
                             uint8_t *chunk = row + ((q ^ (ch & 7)) << 4);
                             if (16 * q >= jv)
                                 *reinterpret_cast<uint4 *>(chunk) = make_uint4(0, 0, 0, 0);
                             else
+#pragma unroll 1
                                 for (int e = jv - 16 * q; e < 16; ++e) chunk[e] = 0;
                         }
                         uint8_t *sfv = smem + S::kSfV + sv * 512 + (ch & 31) * 16 + (ch >> 5) * 4;
+#pragma unroll 1
                         for (int q = (jv + 31) >> 5; q < 4; ++q) sfv[q] = 0;
                     }
                     fence_proxy_async_smem();
@@ -1032,12 +1069,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const uint32_t tD = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kPxColD;
         int k = 0;
         bool ok = true;
+#pragma unroll 1
         for (int c = 0; ok; ++c) {
             ok = __all_sync(0xffffffffu, unit_wait(c));
             const int n = 2 * unit_at(c)->T;
             if (!ok || n == 0) break;
             __syncwarp();
             if (lane == 0) unit_done(c);
+#pragma unroll 1
             for (int i = 0; i < n; ++i, ++k) {
                 const int slot = k & (kPxVSlots - 1);
                 ok = wait(S::kVEmpty + 8 * slot, ((k / kPxVSlots) & 1) ^ 1);
