@@ -1010,8 +1010,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < T; ++i, ++g) {
                 const int sv = g & (kPxVStages - 1);
-                ok = wait_warp(S::kRawFull + 8 * sv, (g / kPxVStages) & 1);
-                if (!ok) break;
+                ok = wait(S::kRawFull + 8 * sv, (g / kPxVStages) & 1);  // one vote, at the tile's end
                 const int jv = reinterpret_cast<const PxTile *>(smem + S::kTiles + 8 * (g & (kPxTiles - 1)))->keys;
                 if (__builtin_expect(jv < 128, 0)) {
                     // Codes past the last token may be anything (a NaN would spread): zeros.
@@ -1041,10 +1040,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {  // 32 tokens, into the halves of D in turn
                         // The four warps have read what the half held (its use before this one).
-                        if ((g > 0 || q > 1) && !wait(S::kDFree + 8 * (q & 1), (q >> 1) ^ 1)) {
-                            ok = false;
-                            break;
-                        }
+                        if (g > 0 || q > 1) ok &= wait(S::kDFree + 8 * (q & 1), (q >> 1) ^ 1);
+                        if (!ok) break;
                         tc_fence_after();
                         px_mma_mxf8(tD + 32 * (q & 1), dRaw + 2 * q, dUnit, px_sf_id(kPxIdD, q),
                                     tSfV | (static_cast<uint32_t>(q) << 30), tOne | (static_cast<uint32_t>(q) << 30));
@@ -1114,10 +1111,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 // Joins the partial results of each query row: those of its unit, one for each share the
 // unit has a part in, in slots unit + share. A CTA takes 32 rows and 32 channels of a unit,
 // a warp four channels, a lane a row, as they are stored; then through shared memory to
-// whole rows. Eight partials are in flight: a unit of few rows and a long prefix has tens.
-constexpr int kMergeBatch = 8;
-__global__ void __launch_bounds__(256) qk4v8_prefix_merge_kernel(const PrefixParams p, __nv_bfloat16 *__restrict__ out,
-                                                                 float *__restrict__ lse) {
+// whole rows. kBatch partials are in flight: 8 where the units are fewer than the shares (a
+// unit has several then; 3.9 us for 18 of them, 9 us one after the other), 2 where they are
+// more, with as many threads again on the SM.
+template <int kBatch>
+__global__ void __launch_bounds__(256, kBatch == 2 ? 6 : 4)
+    qk4v8_prefix_merge_kernel(const PrefixParams p, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
     __shared__ uint2 tile[32][9];  // [row][chunk], 4 bf16
     const int un = static_cast<int>(blockIdx.x >> 4);
     const int row0 = (blockIdx.x >> 2 & 3) * 32;  // of the unit
@@ -1139,11 +1138,11 @@ __global__ void __launch_bounds__(256) qk4v8_prefix_merge_kernel(const PrefixPar
         const float *lp = p.part_lse + static_cast<int64_t>(un + c0) * 128 + row;
         const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + static_cast<int64_t>(un + c0) * (32 * 128) +
                            (chunk0 + warp) * 128 + row;
-        for (int s0 = 0; s0 < np; s0 += kMergeBatch) {
-            float l[kMergeBatch];
-            float4 v[kMergeBatch];
+        for (int s0 = 0; s0 < np; s0 += kBatch) {
+            float l[kBatch];
+            float4 v[kBatch];
 #pragma unroll
-            for (int s = 0; s < kMergeBatch; ++s) {
+            for (int s = 0; s < kBatch; ++s) {
                 l[s] = -INFINITY;
                 v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (s0 + s < np) {
@@ -1153,14 +1152,14 @@ __global__ void __launch_bounds__(256) qk4v8_prefix_merge_kernel(const PrefixPar
             }
             float top = m;
 #pragma unroll
-            for (int s = 0; s < kMergeBatch; ++s) top = fmaxf(top, l[s]);
+            for (int s = 0; s < kBatch; ++s) top = fmaxf(top, l[s]);
             if (top == -INFINITY) continue;
             const float w0 = exp2f(m - top);
             m = top;
             sum *= w0;
             acc.x *= w0, acc.y *= w0, acc.z *= w0, acc.w *= w0;
 #pragma unroll
-            for (int s = 0; s < kMergeBatch; ++s) {
+            for (int s = 0; s < kBatch; ++s) {
                 const float w = exp2f(l[s] - m);
                 sum += w;
                 acc.x += w * v[s].x;
@@ -1202,8 +1201,12 @@ cudaError_t launch_prefix(const CUtensorMap &pk, const CUtensorMap &pv, const CU
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    qk4v8_prefix_merge_kernel<<<16u * static_cast<unsigned>(p.row_tiles) * static_cast<unsigned>(p.Hkv), 256, 0, stream>>>(
-        p, static_cast<__nv_bfloat16 *>(out), lse);
+    const unsigned units = static_cast<unsigned>(p.row_tiles) * static_cast<unsigned>(p.Hkv);
+    auto *o = static_cast<__nv_bfloat16 *>(out);
+    if (units < static_cast<unsigned>(p.shares))
+        qk4v8_prefix_merge_kernel<8><<<16u * units, 256, 0, stream>>>(p, o, lse);
+    else
+        qk4v8_prefix_merge_kernel<2><<<16u * units, 256, 0, stream>>>(p, o, lse);
     return cudaGetLastError();
 }
 
