@@ -47,35 +47,46 @@ __global__ void __launch_bounds__(256, 3) quantize_qk_rope_kernel(const __grid_c
     rope_load<kAdjacent>(a.rope, b, t, a.start ? a.start[b] : 0, j, live, a.status, g);
     int k0, k1;
     rope_chunks(kAdjacent, nrot, j, k0, k1);
-    const __nv_bfloat16 *xt = a.x + b * a.sb + static_cast<int64_t>(t) * a.ss;
     const int nblk = a.cap / 128;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     int h = hc * a.tile.heads + (slot & (hs - 1));
+    // The lane's two chunks of head h, its code words and scales: each step goes hs heads on.
+    const __nv_bfloat16 *x0 = a.x + b * a.sb + static_cast<int64_t>(t) * a.ss + h * a.sh + k0 * 8;
+    const int64_t xstep = hs * a.sh;
+    const int xsecond = (k1 - k0) * 8;
+    const int64_t head = static_cast<int64_t>(b) * a.H + h;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.codes + (head * a.cap + t) * 64) + j;
+    const int64_t cstep = static_cast<int64_t>(hs) * a.cap * 16;
+    uint32_t *dsf = reinterpret_cast<uint32_t *>(a.scales + (head * nblk + t / 128) * 512 + (t & 31) * 16 +
+                                                 ((t & 127) >> 5) * 4);
+    const int64_t sstep = static_cast<int64_t>(hs) * nblk * 128;
     uint4 r0 = zero, r1 = zero;
     if (live && h < h_end) {
-        r0 = *reinterpret_cast<const uint4 *>(xt + h * a.sh + k0 * 8);
-        r1 = *reinterpret_cast<const uint4 *>(xt + h * a.sh + k1 * 8);
+        r0 = *reinterpret_cast<const uint4 *>(x0);
+        r1 = *reinterpret_cast<const uint4 *>(x0 + xsecond);
     }
-    // The trip count is the same for all lanes of the warp (its row helpers shuffle).
-    for (int h0 = hc * a.tile.heads; h0 < h_end; h0 += hs, h += hs) {
+    const bool store = t < a.row_len;
+    // The trip count is the same for all lanes of the warp (its row helpers shuffle). Padding
+    // stays zero on the way through: zero codes and scales.
+    for (int h0 = hc * a.tile.heads; h0 < h_end; h0 += hs) {
         uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-        r0 = r1 = zero;
-        if (live && h + hs < h_end) {  // the next heads' rows, while these are encoded
-            r0 = *reinterpret_cast<const uint4 *>(xt + (h + hs) * a.sh + k0 * 8);
-            r1 = *reinterpret_cast<const uint4 *>(xt + (h + hs) * a.sh + k1 * 8);
+        const bool mine = h < h_end;
+        h += hs;
+        x0 += xstep;
+        if (live && h < h_end) {  // the next heads' rows, while these are encoded
+            r0 = *reinterpret_cast<const uint4 *>(x0);
+            r1 = *reinterpret_cast<const uint4 *>(x0 + xsecond);
         }
         rope_row<kAdjacent>(g, nrot, j, w0, w1);
         uint32_t c0, c1, sf;
         mxfp4_row8<kHadamard>(w0, w1, j, c0, c1, sf);
-        if (t < a.row_len && h < h_end) {
-            const int64_t head = static_cast<int64_t>(b) * a.H + h;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(a.codes + (head * a.cap + t) * 64);
-            dst[j] = live ? c0 : 0u;
-            dst[j + 8] = live ? c1 : 0u;
-            if (j == 0)
-                *reinterpret_cast<uint32_t *>(a.scales + (head * nblk + t / 128) * 512 + (t & 31) * 16 +
-                                              ((t & 127) >> 5) * 4) = live ? sf : 0u;
+        if (store && mine) {
+            dst[0] = c0;
+            dst[8] = c1;
+            if (j == 0) *dsf = sf;
         }
+        dst += cstep;
+        dsf += sstep;
     }
 }
 

@@ -15,7 +15,7 @@
 // remainder e from a fused multiply-add, y = fma(x_a, c, -p) - e is within two
 // units in the last place of fp32, and rounds to the same bf16 value unless it
 // lies within 4 such units of a border between two (9 of 65536 values); those
-// lanes, and lanes with a result that is not finite, redo their 8 pairs in fp64.
+// pairs, and all of a lane with a result that is not finite, are done again in fp64.
 // The bf16 rounding itself is part of the operator: a model that rotates in
 // its bf16 activations and then quantizes gets the same bytes.
 #pragma once
@@ -126,38 +126,47 @@ __device__ __forceinline__ void rotate_pair_f64(float a, float b, float c, float
     yb = __double2float_rn(__dadd_rn(__dmul_rn(db, dc), __dmul_rn(da, ds)));
 }
 
-// Rotates the lane's eight pairs: a[i], b[i] the pairs' two values, as (2i, 2i + 1).
-__device__ __forceinline__ void rotate_pairs(const RopeTrig &g, float2 (&a)[4], float2 (&b)[4]) {
-    float2 ya[4], yb[4];
-    uint32_t near = 0xFFFFFFFFu;  // least distance from a bf16 border, per half, offset to 0..8
-    uint32_t big = 0;             // largest magnitude
+// Two bf16 magnitudes' maximum, twice (signs are not defined); a NaN stays one.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Rotates the lane's eight pairs: a[i], b[i] the pairs' two values, as (2i, 2i + 1); wa, wb: the
+// rotated ones, in bf16.
+__device__ __forceinline__ void rotate_pairs(const RopeTrig &g, const float2 (&a)[4], const float2 (&b)[4],
+                                             uint32_t (&wa)[4], uint32_t (&wb)[4]) {
+    uint32_t near[4];  // least distance from a bf16 border, per half, offset to 0..8
+    uint32_t big = 0;  // largest magnitude
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 c = g.c[i], s = g.s[i], ns = make_float2(-s.x, -s.y);
         // x_a c - x_b s: np = -fl(x_b s); fma(x_b, s, np) is what fl() lost.
         const float2 np = fmul2(b[i], ns);
-        ya[i] = fsub2(ffma2(a[i], c, np), ffma2(b[i], s, np));
+        const float2 ya = fsub2(ffma2(a[i], c, np), ffma2(b[i], s, np));
         // x_b c + x_a s: p = fl(x_a s); fma(x_a, -s, p) is -(what fl() lost).
         const float2 p = fmul2(a[i], s);
-        yb[i] = fsub2(ffma2(b[i], c, p), ffma2(a[i], ns, p));
-        const uint32_t wa = __byte_perm(__float_as_uint(ya[i].x), __float_as_uint(ya[i].y), 0x5410);
-        const uint32_t wb = __byte_perm(__float_as_uint(yb[i].x), __float_as_uint(yb[i].y), 0x5410);
-        near = __viaddmin_u16x2(wa, 0x80048004u, near);
-        near = __viaddmin_u16x2(wb, 0x80048004u, near);
-        big = max(big, max(max(__float_as_uint(ya[i].x) & 0x7FFFFFFFu, __float_as_uint(ya[i].y) & 0x7FFFFFFFu),
-                           max(__float_as_uint(yb[i].x) & 0x7FFFFFFFu, __float_as_uint(yb[i].y) & 0x7FFFFFFFu)));
+        const float2 yb = fsub2(ffma2(b[i], c, p), ffma2(a[i], ns, p));
+        const uint32_t na = __vadd2(__byte_perm(__float_as_uint(ya.x), __float_as_uint(ya.y), 0x5410), 0x80048004u);
+        near[i] = __viaddmin_u16x2(__byte_perm(__float_as_uint(yb.x), __float_as_uint(yb.y), 0x5410), 0x80048004u, na);
+        wa[i] = pack_bf16(ya.x, ya.y);
+        wb[i] = pack_bf16(yb.x, yb.y);
+        big = i == 0 ? max_abs_bf16x2(wa[i], wb[i]) : max_abs_bf16x2(max_abs_bf16x2(wa[i], wb[i]), big);
     }
-    if ((near & 0xFFFFu) <= 8u || (near >> 16) <= 8u || big >= 0x7F800000u) {
+    // (A result that is not finite in fp32 is not in bf16 either.)
+    const bool odd = (big & 0x7F80u) == 0x7F80u || (big & 0x7F800000u) == 0x7F800000u;
+    const uint32_t least = __vminu2(__vminu2(near[0], near[1]), __vminu2(near[2], near[3]));
+    if (odd || (least & 0xFFFFu) <= 8u || (least >> 16) <= 8u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            rotate_pair_f64(a[i].x, b[i].x, g.c[i].x, g.s[i].x, ya[i].x, yb[i].x);
-            rotate_pair_f64(a[i].y, b[i].y, g.c[i].y, g.s[i].y, ya[i].y, yb[i].y);
+            if (!odd && (near[i] & 0xFFFFu) > 8u && (near[i] >> 16) > 8u) continue;
+            float2 ya, yb;
+            rotate_pair_f64(a[i].x, b[i].x, g.c[i].x, g.s[i].x, ya.x, yb.x);
+            rotate_pair_f64(a[i].y, b[i].y, g.c[i].y, g.s[i].y, ya.y, yb.y);
+            wa[i] = pack_bf16(ya.x, ya.y);
+            wb[i] = pack_bf16(yb.x, yb.y);
         }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a[i] = ya[i];
-        b[i] = yb[i];
     }
 }
 
@@ -183,22 +192,23 @@ __device__ __forceinline__ void rope_row(const RopeTrig &g, int nrot, int j, uin
                 b[i] = make_float2(bf16_lo(w1[i]), bf16_hi(w1[i]));
             }
         }
-        rotate_pairs(g, a, b);
+        uint32_t wa[4], wb[4];
+        rotate_pairs(g, a, b, wa, wb);
         if (kAdjacent) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                w0[2 * i] = pack_bf16(a[i].x, b[i].x);
-                w0[2 * i + 1] = pack_bf16(a[i].y, b[i].y);
+                w0[2 * i] = __byte_perm(wa[i], wb[i], 0x5410);
+                w0[2 * i + 1] = __byte_perm(wa[i], wb[i], 0x7632);
                 if (g.hi) {  // the second chunk may pass through
-                    w1[2 * i] = pack_bf16(a[i + 2].x, b[i + 2].x);
-                    w1[2 * i + 1] = pack_bf16(a[i + 2].y, b[i + 2].y);
+                    w1[2 * i] = __byte_perm(wa[i + 2], wb[i + 2], 0x5410);
+                    w1[2 * i + 1] = __byte_perm(wa[i + 2], wb[i + 2], 0x7632);
                 }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                w0[i] = pack_bf16(a[i].x, a[i].y);
-                w1[i] = pack_bf16(b[i].x, b[i].y);
+                w0[i] = wa[i];
+                w1[i] = wb[i];
             }
         }
     }
@@ -287,12 +297,10 @@ __device__ __forceinline__ void mxfp4_row8(const uint32_t (&w0)[4], const uint32
         }
         e = (m0 >> 23) | ((m1 >> 23) << 16);
     } else {
-        uint32_t m0 = 0, m1 = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            m0 = __vmaxu2(m0, w0[i] & 0x7FFF7FFFu);
-            m1 = __vmaxu2(m1, w1[i] & 0x7FFF7FFFu);
-        }
+        const uint32_t m0 =
+            max_abs_bf16x2(max_abs_bf16x2(w0[0], w0[1]), max_abs_bf16x2(w0[2], w0[3])) & 0x7FFF7FFFu;
+        const uint32_t m1 =
+            max_abs_bf16x2(max_abs_bf16x2(w1[0], w1[1]), max_abs_bf16x2(w1[2], w1[3])) & 0x7FFF7FFFu;
         const uint32_t lo = __byte_perm(m0, m1, 0x5410), hi = __byte_perm(m0, m1, 0x7632);
         e = (__vmaxu2(lo, hi) >> 7) & 0x00FF00FFu;
     }
@@ -302,9 +310,11 @@ __device__ __forceinline__ void mxfp4_row8(const uint32_t (&w0)[4], const uint32
     const int X0 = max(static_cast<int>(e & 0xFFFFu) - 129, -127), X1 = max(static_cast<int>(e >> 16) - 129, -127);
     const float f0 = pow2_neg(X0), f1 = pow2_neg(X1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v0[i] *= f0;
-        v1[i] *= f1;
+    for (int i = 0; i < 8; i += 2) {
+        const float2 a = fmul2(make_float2(v0[i], v0[i + 1]), make_float2(f0, f0));
+        const float2 b = fmul2(make_float2(v1[i], v1[i + 1]), make_float2(f1, f1));
+        v0[i] = a.x, v0[i + 1] = a.y;
+        v1[i] = b.x, v1[i + 1] = b.y;
     }
     c0 = cvt_e2m1x8(v0);
     c1 = cvt_e2m1x8(v1);
