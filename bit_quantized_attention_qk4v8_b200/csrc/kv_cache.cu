@@ -251,7 +251,7 @@ struct KvAppendRopeArgs {
     int32_t *status;
     RopeParams rope;
     RopeTiling tile;
-    int64_t k_ctas;
+    uint32_t v_ratio;  // ceil(2^32 * V pages' CTAs / all CTAs)
     int v_pages;  // pages that n tokens can touch
 };
 
@@ -265,70 +265,77 @@ __device__ __forceinline__ int append_count(const KvAppendRopeArgs &a, int b) {
 }
 
 template <bool kAdjacent, bool kHadamard>
-__device__ __forceinline__ void append_k_rows(const KvAppendRopeArgs &a) {
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+__device__ __forceinline__ void append_k_rows(const KvAppendRopeArgs &a, uint32_t cta) {
+    const int item = static_cast<int>(cta * 8 + (threadIdx.x >> 5));
     const int per_b = a.tile.token_groups * a.tile.head_chunks;
-    const int b = static_cast<int>(item / per_b);
+    const int b = item / per_b;
     if (b >= a.B) return;
-    const int rem = static_cast<int>(item - static_cast<int64_t>(b) * per_b);
+    const int rem = item - b * per_b;
     const int tg = rem / a.tile.head_chunks, hc = rem - tg * a.tile.head_chunks;
     const int lane = threadIdx.x & 31, j = lane & 7, slot = lane >> 3;
     const int hs = 1 << a.tile.hs_log2;
     const int t = tg * (4 >> a.tile.hs_log2) + (slot >> a.tile.hs_log2);
     const int h_end = min(a.H, (hc + 1) * a.tile.heads);
     const int L0 = a.seqlens[b];
-    int page = -1;
+    const int nrot = a.rope.rotary >> 4;
+    int k0, k1;
+    rope_chunks(kAdjacent, nrot, j, k0, k1);
+    // The lane's two chunks of head h; each step goes hs heads on. The first are read before
+    // the page and the position are known.
+    int h = hc * a.tile.heads + (slot & (hs - 1));
+    const __nv_bfloat16 *x0 = a.k + b * a.ksb + static_cast<int64_t>(t) * a.kst + h * a.ksh + k0 * 8;
+    const int64_t xstep = hs * a.ksh;
+    const int xsecond = (k1 - k0) * 8;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 r0 = zero, r1 = zero;
     const bool mine = t < append_count(a, b);
+    if (mine && h < h_end) {
+        r0 = *reinterpret_cast<const uint4 *>(x0);
+        r1 = *reinterpret_cast<const uint4 *>(x0 + xsecond);
+    }
+    int page = -1;
     // (L0 + t cannot pass 2^31 within the pages: L0 < max_pages * 128 < 2^31 - n.)
     if (mine) {
         page = L0 <= a.max_pages * 128 ? page_of(a.block_table, a.max_pages, a.num_pages, b, L0 < 0 ? -1 : L0 + t) : -1;
         if (page < 0 && j == 0) flag_bad_page(a.status);
     }
     const bool live = page >= 0;
-    const int nrot = a.rope.rotary >> 4;
     RopeTrig g;
     rope_load<kAdjacent>(a.rope, b, t, L0, j, live, a.status, g);
-    int k0, k1;
-    rope_chunks(kAdjacent, nrot, j, k0, k1);
-    const __nv_bfloat16 *xt = a.k + b * a.ksb + static_cast<int64_t>(t) * a.kst;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    int h = hc * a.tile.heads + (slot & (hs - 1));
-    uint4 r0 = zero, r1 = zero;
-    if (live && h < h_end) {
-        r0 = *reinterpret_cast<const uint4 *>(xt + h * a.ksh + k0 * 8);
-        r1 = *reinterpret_cast<const uint4 *>(xt + h * a.ksh + k1 * 8);
-    }
     const int rr = (L0 + t) & 127;
-    for (int h0 = hc * a.tile.heads; h0 < h_end; h0 += hs, h += hs) {
+    const int64_t row = static_cast<int64_t>(page) * a.H + h;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.k_codes + (row * 128 + rr) * 64) + j;
+    uint32_t *dsf = reinterpret_cast<uint32_t *>(a.k_scales + row * 512 + (rr & 31) * 16 + (rr >> 5) * 4);
+    for (int h0 = hc * a.tile.heads; h0 < h_end; h0 += hs) {
         uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-        r0 = r1 = zero;
-        if (live && h + hs < h_end) {
-            r0 = *reinterpret_cast<const uint4 *>(xt + (h + hs) * a.ksh + k0 * 8);
-            r1 = *reinterpret_cast<const uint4 *>(xt + (h + hs) * a.ksh + k1 * 8);
+        const bool store = live && h < h_end;
+        h += hs;
+        x0 += xstep;
+        if (live && h < h_end) {
+            r0 = *reinterpret_cast<const uint4 *>(x0);
+            r1 = *reinterpret_cast<const uint4 *>(x0 + xsecond);
         }
         rope_row<kAdjacent>(g, nrot, j, w0, w1);
         uint32_t c0, c1, sf;
         mxfp4_row8<kHadamard>(w0, w1, j, c0, c1, sf);
-        if (live && h < h_end) {
-            const int64_t row = static_cast<int64_t>(page) * a.H + h;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(a.k_codes + (row * 128 + rr) * 64);
-            dst[j] = c0;
-            dst[j + 8] = c1;
-            if (j == 0)
-                *reinterpret_cast<uint32_t *>(a.k_scales + row * 512 + (rr & 31) * 16 + (rr >> 5) * 4) = sf;
+        if (store) {
+            dst[0] = c0;
+            dst[8] = c1;
+            if (j == 0) *dsf = sf;
         }
+        dst += hs * (128 * 16);
+        dsf += hs * 128;
     }
 }
 
-__device__ __forceinline__ void append_v_page(const KvAppendRopeArgs &a, int64_t idx) {
+__device__ __forceinline__ void append_v_page(const KvAppendRopeArgs &a, int idx) {
     constexpr int kPitch = 136;   // bf16 elements per staged token row (16 bytes of padding)
     constexpr int kCPitch = 144;  // bytes per staged code row
     __shared__ __align__(16) uint16_t tile[128 * kPitch];
     __shared__ __align__(4) uint8_t atom[512];
     uint8_t *ctile = reinterpret_cast<uint8_t *>(tile);
-    const int64_t bh = idx / a.v_pages;
-    const int pg = static_cast<int>(idx - bh * a.v_pages);
-    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
+    const int bh = idx / a.v_pages, pg = idx - bh * a.v_pages;
+    const int b = bh / a.H, h = bh - b * a.H;
     const int L0 = a.seqlens[b];
     const int m = append_count(a, b);
     if (pg == 0 && h == 0 && threadIdx.x == 0 && a.seqlens_out) a.seqlens_out[b] = L0 + m;
@@ -440,10 +447,12 @@ __device__ __forceinline__ void append_v_page(const KvAppendRopeArgs &a, int64_t
 
 template <bool kAdjacent, bool kHadamard>
 __global__ void __launch_bounds__(256, 3) kv_append_rope_kernel(const __grid_constant__ KvAppendRopeArgs a) {
-    if (blockIdx.x < a.k_ctas)
-        append_k_rows<kAdjacent, kHadamard>(a);
+    // The V pages' CTAs lie evenly among the K rows': those wait for memory, these for the ALU.
+    const uint32_t v = __umulhi(blockIdx.x, a.v_ratio);
+    if (__umulhi(blockIdx.x + 1, a.v_ratio) == v)
+        append_k_rows<kAdjacent, kHadamard>(a, blockIdx.x - v);
     else
-        append_v_page(a, static_cast<int64_t>(blockIdx.x) - a.k_ctas);
+        append_v_page(a, static_cast<int>(v));
 }
 
 // seqlens[b] += new_lens[b] (held to 0..n) in place, after every reader of seqlens ran.
@@ -485,11 +494,12 @@ cudaError_t launch_kv_append_rope(const void *k, const void *v, int B, int n, in
     a.status = status;
     a.rope = rope;
     a.tile = rope_tiling(B, n, H);
-    const int64_t per_b = static_cast<int64_t>(a.tile.token_groups) * a.tile.head_chunks;
-    a.k_ctas = (B * per_b + 7) / 8;
+    const int64_t items = static_cast<int64_t>(B) * a.tile.token_groups * a.tile.head_chunks;
     a.v_pages = (n + 126) / 128 + 1;
-    const int64_t grid = a.k_ctas + static_cast<int64_t>(B) * H * a.v_pages;
-    if (per_b >= (int64_t{1} << 31) || grid >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+    const int64_t v_ctas = static_cast<int64_t>(B) * H * a.v_pages, grid = (items + 7) / 8 + v_ctas;
+    // (Past these, K alone would be 500 GB.)
+    if (items >= (int64_t{1} << 31) - 8 || grid >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+    a.v_ratio = static_cast<uint32_t>(((static_cast<uint64_t>(v_ctas) << 32) + grid - 1) / grid);
     const unsigned g = static_cast<unsigned>(grid);
     if (rope.adjacent) {
         if (hadamard_k)

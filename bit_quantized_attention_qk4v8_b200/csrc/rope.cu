@@ -29,11 +29,11 @@ struct QkRopeArgs {
 // One warp per item (batch entry, TS tokens, up to 32 heads), eight lanes per row.
 template <bool kAdjacent, bool kHadamard>
 __global__ void __launch_bounds__(256, 3) quantize_qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int item = static_cast<int>(blockIdx.x * 8 + (threadIdx.x >> 5));
     const int per_b = a.tile.token_groups * a.tile.head_chunks;
-    const int b = static_cast<int>(item / per_b);
+    const int b = item / per_b;
     if (b >= a.B) return;
-    const int rem = static_cast<int>(item - static_cast<int64_t>(b) * per_b);
+    const int rem = item - b * per_b;
     const int tg = rem / a.tile.head_chunks, hc = rem - tg * a.tile.head_chunks;
     const int lane = threadIdx.x & 31, j = lane & 7, slot = lane >> 3;
     const int hs = 1 << a.tile.hs_log2;
@@ -112,10 +112,9 @@ cudaError_t launch_quantize_qk_rope(const void *x, int B, int S, int H, int64_t 
     a.rope = rope;
     if (a.row_len == 0) return cudaSuccess;
     a.tile = rope_tiling(B, a.row_len, H);
-    const int64_t per_b = static_cast<int64_t>(a.tile.token_groups) * a.tile.head_chunks;
-    const int64_t grid = (B * per_b + 7) / 8;
-    if (per_b >= (int64_t{1} << 31) || grid >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
-    const unsigned n = static_cast<unsigned>(grid);
+    const int64_t items = static_cast<int64_t>(B) * a.tile.token_groups * a.tile.head_chunks;
+    if (items >= (int64_t{1} << 31) - 8) return cudaErrorInvalidValue;  // (500 GB of rows)
+    const unsigned n = static_cast<unsigned>((items + 7) / 8);
     if (rope.adjacent) {
         if (rotate)
             quantize_qk_rope_kernel<true, true><<<n, 256, 0, stream>>>(a);
