@@ -599,10 +599,11 @@ def quantize_qk_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tens
         out = MXFP4(torch.empty((B, H, cap, 64), dtype=torch.uint8, device=dev),
                     torch.empty((B, H, cap // 128, 512), dtype=torch.uint8, device=dev), B, H, cap, T)
     with _on(dev):
-        check(lib().qk4v8_quantize_qk_rope(x.data_ptr(), B, T, H, D, x.stride(0), x.stride(1), x.stride(2), _ptr(sl), st,
-                                           ctypes.addressof(rs), int(bool(hadamard)), cap, int(bool(pad)),
-                                           out.codes.data_ptr(), out.scales.data_ptr(), _ptr(dev_status),
-                                           _stream(dev)), "qk4v8_quantize_qk_rope")
+        # (An empty x has a null pointer; no row of it is read.)
+        check(lib().qk4v8_quantize_qk_rope(x.data_ptr() or out.codes.data_ptr(), B, T, H, D, x.stride(0), x.stride(1),
+                                           x.stride(2), _ptr(sl), st, ctypes.addressof(rs), int(bool(hadamard)), cap,
+                                           int(bool(pad)), out.codes.data_ptr(), out.scales.data_ptr(),
+                                           _ptr(dev_status), _stream(dev)), "qk4v8_quantize_qk_rope")
     out.length = T
     return out
 

@@ -1164,15 +1164,19 @@ int plan_prefix(int B, int Hq, int Hkv, int nq, int prefix_len, int max_seqlen, 
     PrefixPlan q;
     const int64_t rows = static_cast<int64_t>(B) * (Hq / Hkv) * nq;
     const int64_t row_tiles = (rows + 127) / 128, units = row_tiles * Hkv;
-    // (Keys: a unit's tiles, of the prefix and of up to 129 sequences, are counted in an int.)
-    if (rows >= (int64_t{1} << 30) || units >= (int64_t{1} << 28) || static_cast<int64_t>(B) * Hq * nq >= (int64_t{1} << 31))
+    // (16 CTAs of the merge for each unit.)
+    if (rows >= (int64_t{1} << 30) || units >= (int64_t{1} << 27) || static_cast<int64_t>(B) * Hq * nq >= (int64_t{1} << 31))
         return set_error(QK4V8_ERR_INVALID_ARG, "too many query rows in one call");
     q.row_tiles = static_cast<int>(row_tiles);
     q.tiles = static_cast<int>((static_cast<int64_t>(prefix_len) + 127) / 128);
     q.own = max_seqlen > 0;
     // Every SM, unless there are fewer tiles than that even with all sequences at their longest.
+    // (A sequence has rows in two row tiles at most. A unit's start counts as a tile.)
     const int64_t own_tiles = (static_cast<int64_t>(max_seqlen) + 127) / 128;
     const int64_t most = q.tiles * units + own_tiles * 2 * B * Hkv + units;
+    if (most >= (int64_t{1} << 30))  // the kernel's count of them is an int
+        return set_error(QK4V8_ERR_INVALID_ARG, "too many key tiles in one call (prefix_len=%d max_seqlen=%d)", prefix_len,
+                         max_seqlen);
     q.shares = q.tiles || q.own ? static_cast<int>(most < sms ? most : sms) : 0;
     const size_t slots = q.shares ? static_cast<size_t>(units) + q.shares : 0;
     auto take = [&](size_t bytes) {
@@ -1311,7 +1315,8 @@ int qk4v8_attention_decode_prefix_paged(const uint8_t *q_codes, const uint8_t *q
                                         int max_pages, const int32_t *seqlens_k, int max_seqlen, int causal_in_block,
                                         float softmax_scale, void *workspace, size_t workspace_bytes, void *out,
                                         float *lse, int32_t *dev_status, void *stream) {
-    if (!block_table || !prefix_table) return set_error(QK4V8_ERR_INVALID_ARG, "block_table or prefix_table is null");
+    if (!block_table || (prefix_len > 0 && !prefix_table))
+        return set_error(QK4V8_ERR_INVALID_ARG, "block_table or prefix_table is null");
     if (max_pages <= 0 || max_pages >= (1 << 24) || num_pages <= 0 || Hkv <= 0 ||
         static_cast<int64_t>(num_pages) * Hkv >= (int64_t{1} << 31))
         return set_error(QK4V8_ERR_INVALID_ARG, "bad page pool: num_pages=%d max_pages=%d", num_pages, max_pages);
