@@ -82,7 +82,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream's handle (without a Stream object around it: 2 us of host time)."""
+    if device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 _HERE = contextlib.nullcontext()
@@ -608,6 +611,9 @@ def quantize_qk_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tens
     return out
 
 
+_Strides = ctypes.c_int64 * 3
+
+
 def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rope: Rope,
                    positions: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
                    seqlens_out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None) -> PagedKV:
@@ -631,8 +637,7 @@ def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rop
     nl = _int32_on(new_lens, B, dev, "new_lens")
     lens = cache.seqlens.data_ptr()
     so = lens if seqlens_out is None else _int32_on(seqlens_out, B, dev, "seqlens_out")
-    strides = ctypes.c_int64 * 3
-    ks, vs = strides(*k_new.stride()[:3]), strides(*v_new.stride()[:3])
+    ks, vs = _Strides(*k_new.stride()[:3]), _Strides(*v_new.stride()[:3])
     with _on(dev):
         check(lib().qk4v8_kv_append_rope(k_new.data_ptr(), v_new.data_ptr(), B, n_new, Hkv, D, ctypes.addressof(ks),
                                          ctypes.addressof(vs), lens, nl, so, ctypes.addressof(rs),

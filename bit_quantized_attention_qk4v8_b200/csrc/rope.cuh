@@ -133,21 +133,39 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
-// Rotates the lane's eight pairs: a[i], b[i] the pairs' two values, as (2i, 2i + 1); wa, wb: the
-// rotated ones, in bf16.
-__device__ __forceinline__ void rotate_pairs(const RopeTrig &g, const float2 (&a)[4], const float2 (&b)[4],
+// Pairs 2i, 2i + 1 of the lane, from its two chunks' words: a, b the pairs' first and second values.
+template <bool kAdjacent>
+__device__ __forceinline__ void unpack_pairs(uint32_t u, uint32_t v, float2 &a, float2 &b) {
+    if (kAdjacent) {  // two words of a chunk
+        a = make_float2(bf16_lo(u), bf16_lo(v));
+        b = make_float2(bf16_hi(u), bf16_hi(v));
+    } else {          // a word of each chunk
+        a = make_float2(bf16_lo(u), bf16_hi(u));
+        b = make_float2(bf16_lo(v), bf16_hi(v));
+    }
+}
+
+// Rotates the lane's eight pairs: wa, wb the rotated first and second values, in bf16.
+template <bool kAdjacent>
+__device__ __forceinline__ void rotate_pairs(const RopeTrig &g, const uint32_t (&w0)[4], const uint32_t (&w1)[4],
                                              uint32_t (&wa)[4], uint32_t (&wb)[4]) {
+    auto word = [&](int i, bool second) {
+        if (!kAdjacent) return second ? w1[i] : w0[i];
+        return i < 2 ? w0[2 * i + second] : w1[2 * (i - 2) + second];
+    };
     uint32_t near[4];  // least distance from a bf16 border, per half, offset to 0..8
     uint32_t big = 0;  // largest magnitude
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 c = g.c[i], s = g.s[i], ns = make_float2(-s.x, -s.y);
+        float2 a, b;
+        unpack_pairs<kAdjacent>(word(i, false), word(i, true), a, b);
         // x_a c - x_b s: np = -fl(x_b s); fma(x_b, s, np) is what fl() lost.
-        const float2 np = fmul2(b[i], ns);
-        const float2 ya = fsub2(ffma2(a[i], c, np), ffma2(b[i], s, np));
+        const float2 np = fmul2(b, ns);
+        const float2 ya = fsub2(ffma2(a, c, np), ffma2(b, s, np));
         // x_b c + x_a s: p = fl(x_a s); fma(x_a, -s, p) is -(what fl() lost).
-        const float2 p = fmul2(a[i], s);
-        const float2 yb = fsub2(ffma2(b[i], c, p), ffma2(a[i], ns, p));
+        const float2 p = fmul2(a, s);
+        const float2 yb = fsub2(ffma2(b, c, p), ffma2(a, ns, p));
         const uint32_t na = __vadd2(__byte_perm(__float_as_uint(ya.x), __float_as_uint(ya.y), 0x5410), 0x80048004u);
         near[i] = __viaddmin_u16x2(__byte_perm(__float_as_uint(yb.x), __float_as_uint(yb.y), 0x5410), 0x80048004u, na);
         wa[i] = pack_bf16(ya.x, ya.y);
@@ -161,9 +179,13 @@ __device__ __forceinline__ void rotate_pairs(const RopeTrig &g, const float2 (&a
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (!odd && (near[i] & 0xFFFFu) > 8u && (near[i] >> 16) > 8u) continue;
-            float2 ya, yb;
-            rotate_pair_f64(a[i].x, b[i].x, g.c[i].x, g.s[i].x, ya.x, yb.x);
-            rotate_pair_f64(a[i].y, b[i].y, g.c[i].y, g.s[i].y, ya.y, yb.y);
+            // Unpacked anew: held for this seldom path, the values would take 16 registers.
+            uint32_t u = word(i, false), v = word(i, true);
+            asm volatile("" : "+r"(u), "+r"(v));
+            float2 a, b, ya, yb;
+            unpack_pairs<kAdjacent>(u, v, a, b);
+            rotate_pair_f64(a.x, b.x, g.c[i].x, g.s[i].x, ya.x, yb.x);
+            rotate_pair_f64(a.y, b.y, g.c[i].y, g.s[i].y, ya.y, yb.y);
             wa[i] = pack_bf16(ya.x, ya.y);
             wb[i] = pack_bf16(yb.x, yb.y);
         }
@@ -176,24 +198,8 @@ __device__ __forceinline__ void rotate_pairs(const RopeTrig &g, const float2 (&a
 template <bool kAdjacent>
 __device__ __forceinline__ void rope_row(const RopeTrig &g, int nrot, int j, uint32_t (&w0)[4], uint32_t (&w1)[4]) {
     if (g.lo) {
-        float2 a[4], b[4];
-        if (kAdjacent) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                a[i] = make_float2(bf16_lo(w0[2 * i]), bf16_lo(w0[2 * i + 1]));
-                b[i] = make_float2(bf16_hi(w0[2 * i]), bf16_hi(w0[2 * i + 1]));
-                a[i + 2] = make_float2(bf16_lo(w1[2 * i]), bf16_lo(w1[2 * i + 1]));
-                b[i + 2] = make_float2(bf16_hi(w1[2 * i]), bf16_hi(w1[2 * i + 1]));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = make_float2(bf16_lo(w0[i]), bf16_hi(w0[i]));
-                b[i] = make_float2(bf16_lo(w1[i]), bf16_hi(w1[i]));
-            }
-        }
         uint32_t wa[4], wb[4];
-        rotate_pairs(g, a, b, wa, wb);
+        rotate_pairs<kAdjacent>(g, w0, w1, wa, wb);
         if (kAdjacent) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
