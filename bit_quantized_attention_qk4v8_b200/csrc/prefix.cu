@@ -109,7 +109,7 @@ struct PxSmem {
     static constexpr int kOFull = kPvDone + 8 * kPxSets, kOFree = kOFull + 8, kDrain = kOFree + 8;
     static constexpr int kUnitFull = kDrain + 8, kUnitEmpty = kUnitFull + 8 * kPxUnits;
     static constexpr int kBarEnd = kUnitEmpty + 8 * kPxUnits;
-    static constexpr int kMisc = (kBarEnd + 15) / 16 * 16;  // TMEM address, abort flag
+    static constexpr int kMisc = (kBarEnd + 15) / 16 * 16;  // TMEM address, abort flag, tile to clear
     static constexpr int kUnits = kMisc + 16;          // PxUnit [kPxUnits]
     static constexpr int kTiles = kUnits + 64 * kPxUnits;   // PxTile [kPxTiles]
     static constexpr int kLens = kTiles + 8 * kPxTiles;     // int [kPxSeqs]: the unit's sequences
@@ -221,7 +221,7 @@ __device__ __forceinline__ bool px_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Bounded wait on an mbarrier phase: false past kWaitTimeoutNs, or once the CTA's abort flag is
+// Bounded wait on an mbarrier phase: false past 2^31 clocks (a second), or once the CTA's abort flag is
 // up. A role whose wait gave up raises the flag at its end (px_give_up), so the others
 // follow at once. A dozen instructions, all of them: with waits of sixty at thirty
 // places the roles' loops left the SM's instruction cache (103 misses a tile, and every
@@ -230,54 +230,54 @@ __device__ __forceinline__ bool px_try(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool px_wait(uint32_t bar, uint32_t parity, uint32_t flag) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t1;\n\t.reg .b32 f;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 t0, t1, f;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "@p bra PX_DONE;\n\t"
-        "mov.u64 t0, %%globaltimer;\n\t"
+        "mov.u32 t0, %%clock;\n\t"
         "PX_AGAIN:\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "@p bra PX_DONE;\n\t"
         "ld.volatile.shared.b32 f, [%3];\n\t"
-        "mov.u64 t1, %%globaltimer;\n\t"
-        "sub.u64 t1, t1, t0;\n\t"
-        "setp.gt.u64 q, t1, %4;\n\t"
+        "mov.u32 t1, %%clock;\n\t"
+        "sub.u32 t1, t1, t0;\n\t"
+        "setp.lt.s32 q, t1, 0;\n\t"
         "setp.ne.or.b32 q, f, 0, q;\n\t"
         "@!q bra PX_AGAIN;\n\t"
         "PX_DONE:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(flag), "n"(kWaitTimeoutNs)
+        : "r"(bar), "r"(parity), "r"(flag)
         : "memory");
     return ok != 0;
 }
 
 // The reference of a row goes from a subtile's owner to the next one's as one 8-byte word with
-// the subtile's number. px_take: false past kWaitTimeoutNs or once the abort flag is up.
+// the subtile's number. px_take: false past 2^31 clocks or once the abort flag is up.
 __device__ __forceinline__ void px_pass(uint32_t at, int seqno, float m) {
     asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(__float_as_uint(m)), "r"(seqno) : "memory");
 }
 __device__ __forceinline__ bool px_take(uint32_t at, int seqno, uint32_t flag, float &m) {
     uint32_t ok, v;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t1;\n\t.reg .b32 f, n;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 t0, t1, f, n;\n\t"
         "ld.volatile.shared.v2.b32 {%1, n}, [%2];\n\t"
         "setp.eq.s32 p, n, %3;\n\t"
         "@p bra PX_DONE;\n\t"
-        "mov.u64 t0, %%globaltimer;\n\t"
+        "mov.u32 t0, %%clock;\n\t"
         "PX_AGAIN:\n\t"
         "ld.volatile.shared.v2.b32 {%1, n}, [%2];\n\t"
         "setp.eq.s32 p, n, %3;\n\t"
         "@p bra PX_DONE;\n\t"
         "ld.volatile.shared.b32 f, [%4];\n\t"
-        "mov.u64 t1, %%globaltimer;\n\t"
-        "sub.u64 t1, t1, t0;\n\t"
-        "setp.gt.u64 q, t1, %5;\n\t"
+        "mov.u32 t1, %%clock;\n\t"
+        "sub.u32 t1, t1, t0;\n\t"
+        "setp.lt.s32 q, t1, 0;\n\t"
         "setp.ne.or.b32 q, f, 0, q;\n\t"
         "@!q bra PX_AGAIN;\n\t"
         "PX_DONE:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok), "=r"(v)
-        : "r"(at), "r"(seqno), "r"(flag), "n"(kWaitTimeoutNs)
+        : "r"(at), "r"(seqno), "r"(flag)
         : "memory");
     m = __uint_as_float(v);
     return ok != 0;
@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // The three issuers, the expanding and the softmax warps.
         init(S::kUnitEmpty, kPxUnits, 3 + 4 + kPxSoftmaxWarps);
         // A status already set by another launch or CTA: unwind at once, uniformly.
+        *reinterpret_cast<uint32_t *>(smem + S::kMisc + 8) = 0;  // no tile to clear
         *abort_flag = (p.status && *reinterpret_cast<const volatile int32_t *>(p.status) != 0) ? 1u : 0u;
         fence_barrier_init();
     }
@@ -572,6 +573,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const uint32_t tmem = *tmem_slot;
     // The announced units: unit c's entry once it is there, and its release.
     auto unit_at = [&](int c) { return reinterpret_cast<const PxUnit *>(smem + S::kUnits + 64 * (c & (kPxUnits - 1))); };
+    auto tile_at = [&](int g) { return reinterpret_cast<const PxTile *>(smem + S::kTiles + 8 * (g & (kPxTiles - 1))); };
     auto unit_wait = [&](int c) { return wait(S::kUnitFull + 8 * (c & (kPxUnits - 1)), (c / kPxUnits) & 1); };
     auto unit_done = [&](int c) { px_arrive(sb + S::kUnitEmpty + 8 * (c & (kPxUnits - 1))); };
 
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 // the subtile's end: a vote after each was a tenth of the loop.)
                 ok = wait(S::kSFull + 8 * set, k & 1);
                 tc_fence_after();
-                const PxTile tile = *reinterpret_cast<const PxTile *>(smem + S::kTiles + 8 * ((gt + (i >> 1)) & (kPxTiles - 1)));
+                const PxTile tile = *tile_at(gt + (i >> 1));
                 const int lo = tile.rows & 0xFF, hi = (tile.rows >> 8) & 0xFF;
                 const bool active = lo < quarter * 32 + 32 && hi > quarter * 32;  // a row of the warp sees it
                 uint32_t s[2][32];
@@ -997,64 +999,54 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // times a unit matrix, which the tensor core expands with their scales.
         const uint32_t tD = tmem + kPxColD, tSfV = tmem + kPxColSfV, tOne = tmem + kPxColOne;
         const uint32_t dUnit = px_desc_lo(sb + S::kUnit, 16);
-        if (lane == 0) px_cp_atom(tOne, px_desc_lo(sb + S::kSfOne, 0));
-        int g = 0;
-        bool ok = true;
+        // (One thread and few instructions a tile: its loop is what the expansion waits for. With
+        // the warp in it, for the tiles that end early, it took 1350 clk from tile to tile.)
+        if (elect_one()) {
+            px_cp_atom(tOne, px_desc_lo(sb + S::kSfOne, 0));
+            int g = 0;
+            uint32_t p0 = 0;  // uses of D's first half so far, mod 2
+            bool ok = true;
 #pragma unroll 1
-        for (int c = 0; ok; ++c) {
-            ok = __all_sync(0xffffffffu, unit_wait(c));
-            const int T = unit_at(c)->T;
-            if (!ok || T == 0) break;
-            __syncwarp();
-            if (lane == 0) unit_done(c);
+            for (int c = 0; ok; ++c) {
+                ok = unit_wait(c);
+                const int T = unit_at(c)->T;
+                if (!ok || T == 0) break;
+                unit_done(c);
 #pragma unroll 1
-            for (int i = 0; i < T; ++i, ++g) {
-                const int sv = g & (kPxVStages - 1);
-                ok = wait(S::kRawFull + 8 * sv, (g / kPxVStages) & 1);  // one vote, at the tile's end
-                const int jv = reinterpret_cast<const PxTile *>(smem + S::kTiles + 8 * (g & (kPxTiles - 1)))->keys;
-                if (__builtin_expect(jv < 128, 0)) {
-                    // Codes past the last token may be anything (a NaN would spread): zeros.
-#pragma unroll 1
-                    for (int ch = lane; ch < 128; ch += 32) {
-                        uint8_t *row = smem + S::kRaw + sv * S::kRawBytes + ch * 128;
-#pragma unroll 1
-                        for (int q = jv >> 4; q < 8; ++q) {
-                            uint8_t *chunk = row + ((q ^ (ch & 7)) << 4);
-                            if (16 * q >= jv)
-                                *reinterpret_cast<uint4 *>(chunk) = make_uint4(0, 0, 0, 0);
-                            else
-#pragma unroll 1
-                                for (int e = jv - 16 * q; e < 16; ++e) chunk[e] = 0;
-                        }
-                        uint8_t *sfv = smem + S::kSfV + sv * 512 + (ch & 31) * 16 + (ch >> 5) * 4;
-#pragma unroll 1
-                        for (int q = (jv + 31) >> 5; q < 4; ++q) sfv[q] = 0;
+                for (int i = 0; i < T; ++i, ++g) {
+                    const int sv = g & (kPxVStages - 1);
+                    ok = wait(S::kRawFull + 8 * sv, (g / kPxVStages) & 1);
+                    // The four warps have read what the half held (its use before this one).
+                    ok &= wait(S::kDFree, p0 ^ 1);
+                    if (!ok) break;
+                    if (__builtin_expect(tile_at(g)->keys < 128, 0)) {
+                        // The expanding warps clear what lies past the last token; they take the
+                        // request for a use of the half.
+                        sts32(sb + S::kMisc + 8, static_cast<uint32_t>(g + 1));
+                        px_arrive(sb + S::kDFull);
+                        p0 ^= 1;
+                        ok = wait(S::kDFree, p0 ^ 1);
+                        if (!ok) break;
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (lane == 0) {
                     tc_fence_after();
                     px_cp_atom(tSfV, px_desc_lo(sb + S::kSfV, 0) + sv * 32);
                     const uint32_t dRaw = px_desc_lo(sb + S::kRaw, 16) + sv * (S::kRawBytes >> 4);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {  // 32 tokens, into the halves of D in turn
-                        // The four warps have read what the half held (its use before this one).
-                        if (g > 0 || q > 1) ok &= wait(S::kDFree + 8 * (q & 1), (q >> 1) ^ 1);
+                        if (q > 0) ok = wait(S::kDFree + 8 * (q & 1), q == 2 ? p0 : q == 1 ? 1u : 0u);
                         if (!ok) break;
                         tc_fence_after();
                         px_mma_mxf8(tD + 32 * (q & 1), dRaw + 2 * q, dUnit, px_sf_id(kPxIdD, q),
                                     tSfV | (static_cast<uint32_t>(q) << 30), tOne | (static_cast<uint32_t>(q) << 30));
                         px_commit(sb + S::kDFull + 8 * (q & 1));
                     }
+                    if (!ok) break;
                     px_commit(sb + S::kRawEmpty + 8 * sv);
                 }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
             }
+            if (!ok) px_give_up(abort_flag, p.status);
+            px_commit(sb + S::kDrain);
         }
-        if (!ok && lane == 0) px_give_up(abort_flag, p.status);
-        if (lane == 0) px_commit(sb + S::kDrain);
         __syncwarp();
     } else {
         // -------------------------------------------------------------- V expansion
@@ -1065,6 +1057,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const int quarter = warp & 3, ch = quarter * 32 + lane;
         const uint32_t tD = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kPxColD;
         int k = 0;
+        uint32_t f0 = 0;  // D's first half: the parity of what comes next
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; ok; ++c) {
@@ -1080,7 +1073,34 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 const uint32_t row = sb + S::kV + slot * S::kVHalf + ch * 128;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {  // while the tensor core expands the other half
-                    ok &= wait(S::kDFull + 8 * q, k & 1);
+                    ok &= wait(S::kDFull + 8 * q, q == 0 ? f0 : k & 1);
+                    if (q == 0) {
+                        f0 ^= 1;
+                        if (__builtin_expect((k & 1) == 0 && lds32(sb + S::kMisc + 8) == (k >> 1) + 1u, 0)) {
+                            // This tile ends early. Codes past the last token may be anything (a NaN
+                            // would spread): zeros, in the thread's channel.
+                            const int sv = (k >> 1) & (kPxVStages - 1), jv = tile_at(k >> 1)->keys;
+                            uint8_t *codes = smem + S::kRaw + sv * S::kRawBytes + ch * 128;
+#pragma unroll 1
+                            for (int at = jv >> 4; at < 8; ++at) {
+                                uint8_t *chunk = codes + ((at ^ (ch & 7)) << 4);
+                                if (16 * at >= jv) {
+                                    *reinterpret_cast<uint4 *>(chunk) = make_uint4(0, 0, 0, 0);
+                                } else {
+#pragma unroll 1
+                                    for (int e = jv - 16 * at; e < 16; ++e) chunk[e] = 0;
+                                }
+                            }
+                            uint8_t *sfv = smem + S::kSfV + sv * 512 + (ch & 31) * 16 + (ch >> 5) * 4;
+#pragma unroll 1
+                            for (int at = (jv + 31) >> 5; at < 4; ++at) sfv[at] = 0;
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) px_arrive(sb + S::kDFree);
+                            ok &= wait(S::kDFull, f0);
+                            f0 ^= 1;
+                        }
+                    }
                     tc_fence_after();
                     uint32_t d[32];
                     tc_ld_32x32b_x32(tD + 32 * q, d);
