@@ -114,7 +114,7 @@ struct PxSmem {
     static constexpr int kTiles = kUnits + 64 * kPxUnits;   // PxTile [kPxTiles]
     static constexpr int kLens = kTiles + 8 * kPxTiles;     // int [kPxSeqs]: the unit's sequences
     static constexpr int kNext = (kLens + 4 * kPxSeqs + 15) / 16 * 16;  // int4 [32]: the next tiles to load
-    static constexpr int kUsed = kNext + 16 * 32;
+    static constexpr int kUsed = kNext + 16 * 32;  // (descriptor, K row, block)
     static constexpr int kBytes = kUsed + 1024;
 };
 static_assert(PxSmem::kK % 1024 == 0 && PxSmem::kV % 1024 == 0 && PxSmem::kVHalf % 1024 == 0 &&
@@ -200,6 +200,12 @@ __device__ __forceinline__ void tc_wait_ld32(uint32_t (&r)[32]) {
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
                    "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
                    "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void tc_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 // One elected thread of the (converged) warp.
@@ -609,6 +615,25 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 const int lo = tile.rows & 0xFF, hi = (tile.rows >> 8) & 0xFF;
                 const bool active = lo < quarter * 32 + 32 && hi > quarter * 32;  // a row of the warp sees it
                 uint32_t s[2][32];
+                // Keys j < jv of the subtile are seen; a row of another sequence sees none.
+                const bool mine = row >= lo && row < hi;
+                int jv = tile.keys - 64 * (i & 1);
+                if (p.causal && (tile.rows >> 16)) jv -= late;
+                if (__builtin_expect(active && __any_sync(0xffffffffu, mine && jv < 64), 0)) {
+                    // Masked in place, in a short loop: unrolled over the registers it took 2.7 KB
+                    // of the instruction cache that all roles share.
+#pragma unroll 1
+                    for (int j0 = 0; j0 < 64; j0 += 16) {
+                        uint32_t v[16];
+                        tc_ld_32x32b_x16(tS + j0, v);
+                        tc_wait_ld16(v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j0 + j >= jv) v[j] = 0xFF800000u;
+                        tc_st_32x32b_x16(tS + j0, v);
+                    }
+                    tc_wait_st();
+                }
                 if (active) {
                     tc_ld_32x32b_x32(tS, s[0]);
                     tc_ld_32x32b_x32(tS + 32, s[1]);
@@ -620,15 +645,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 if (lane == 0) px_arrive(sb + S::kSFree + 8 * set);  // the next S of this set, while P is computed
                 float hm = -INFINITY;
                 if (active) {
-                    // Keys j < jv of the subtile are seen; a row of another sequence sees none.
-                    int jv = tile.keys - 64 * (i & 1);
-                    if (p.causal && (tile.rows >> 16)) jv -= late;
-                    const bool mine = row >= lo && row < hi;
-                    if (__builtin_expect(__any_sync(0xffffffffu, mine && jv < 64), 0)) {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (j >= jv) s[j >> 5][j & 31] = 0xFF800000u;
-                    }
                     hm = sc * fmaxf(max32(s[0]), max32(s[1]));
                     if (!mine) hm = -INFINITY;
                 }
@@ -706,14 +722,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 // [slot][32 chunks of 4 channels][128 rows][4]: a warp stores its 32 rows side by side.
                 float4 *dst = reinterpret_cast<float4 *>(p.part_o) + slot * (32 * 128) + row;
 #pragma unroll 1
-                for (int q = set; q < 4; q += kPxSets) {  // 32 channels at a time
-                    uint32_t o[32];
-                    tc_ld_32x32b_x32(tmem + lane_base + kPxColO + 32 * q, o);
-                    tc_wait_ld32(o);
+                for (int q = set; q < 8; q += kPxSets) {  // 16 channels at a time: 3, 3 and 2 for the sets
+                    uint32_t o[16];
+                    tc_ld_32x32b_x16(tmem + lane_base + kPxColO + 16 * q, o);
+                    tc_wait_ld16(o);
                     if (row < u.rows) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[(8 * q + e) * 128] =
+                        for (int e = 0; e < 4; ++e)
+                            dst[(4 * q + e) * 128] =
                                 make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                                             __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
                     }
@@ -799,20 +815,19 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 walk(b0, b1, mine);
                 int row, blk;
                 px_tile(p, u.h, seq, tile, row, blk);
-                next[mine] = make_int4(seq, row, blk, len - tile * 128);
+                // Rows of the row tile that see it, keys from its first on, K/V row and block.
+                const bool sees = seq < 0;  // all rows do
+                const int lo = sees ? 0 : imax(seq * p.gq - u.row0, 0), hi = sees ? 128 : imin((seq + 1) * p.gq - u.row0, 128);
+                next[mine] = make_int4(lo | (hi << 8) | (sees ? 0 : 1 << 16), len - tile * 128, row, blk);
                 walk(b0, b1, n - mine);
                 __syncwarp();
                 if (lane == 0) {
 #pragma unroll 1
                     for (int i = 0; i < n; ++i) {
                         const int4 d = next[i];
-                        const bool own = d.x >= 0;
-                        // Rows of the row tile that see it.
-                        const int lo = own ? imax(d.x * p.gq - u.row0, 0) : 0;
-                        const int hi = own ? imin((d.x + 1) * p.gq - u.row0, 128) : 128;
-                        const PxTile t{lo | (hi << 8) | (own ? 1 << 16 : 0), d.w};
+                        const bool own = (d.x >> 16) != 0;
                         const CUtensorMap *mk = own ? &tmap_k : &tmap_pk, *mv = own ? &tmap_v : &tmap_pv;
-                        const int vt = d.y * (own ? p.own_blocks : p.prefix_blocks) + d.z;
+                        const int vt = d.z * (own ? p.own_blocks : p.prefix_blocks) + d.w;
                         const int64_t at = static_cast<int64_t>(vt) * 512;
                         const int gi = k_issued;
                         const int st = gi & (kPxKStages - 1), sv = gi & (kPxVStages - 1);
@@ -822,9 +837,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                         if (!ok) break;
                         // (The tile eight before is done with: S of the one four before is in the
                         // tensor core's past, so every set has gone on from the eighth.)
-                        *reinterpret_cast<PxTile *>(smem + S::kTiles + 8 * (gi & (kPxTiles - 1))) = t;
+                        *reinterpret_cast<PxTile *>(smem + S::kTiles + 8 * (gi & (kPxTiles - 1))) = PxTile{d.x, d.y};
                         mbar_arrive_expect_tx(kf, S::kKBytes + 512);
-                        tma_load_3d(smem + S::kK + st * S::kKBytes, mk, 0, d.z * 128, d.y, kf);
+                        tma_load_3d(smem + S::kK + st * S::kKBytes, mk, 0, d.w * 128, d.z, kf);
                         bulk_load(smem + S::kSfK + st * 512, (own ? p.k_scales : p.p_k_scales) + at, 512, kf);
                         k_issued = gi + 1;
                         ok = wait(S::kRawEmpty + 8 * sv, ((gi / kPxVStages) & 1) ^ 1);
@@ -927,7 +942,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     tc_fence_after();
                     px_cp_atom(tSfK, px_desc_lo(sb + S::kSfK, 0) + st * 32);
                     const uint32_t dK = px_desc_lo(sb + S::kK, 16) + st * (S::kKBytes >> 4);
-#pragma unroll
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         ok = wait(S::kSFree + 8 * set, sph);
                         if (!ok) break;
