@@ -66,7 +66,7 @@ namespace {
 constexpr int kPxKStages = 4;
 constexpr int kPxVStages = 4;
 constexpr int kPxVSlots = 4;                // 64 tokens of expanded V each
-constexpr int kPxSets = 3;
+constexpr int kPxSets = 2;
 constexpr int kPxUnits = 8;                 // units announced at most
 constexpr int kPxTiles = 8;                 // tiles described at most
 constexpr int kPxSeqs = 132;                // sequences with rows among 128 consecutive ones: up to 129
@@ -76,7 +76,7 @@ constexpr int kPxQkWarp = kPxFeedWarp + 1;
 constexpr int kPxDWarp = kPxFeedWarp + 2;
 constexpr int kPxPvWarp = kPxFeedWarp + 3;
 constexpr int kPxExpandWarp = kPxSoftmaxWarps + 4;
-constexpr int kPxThreads = 32 * (kPxExpandWarp + 4);
+constexpr int kPxThreads = 32 * (kPxExpandWarp + 8);
 constexpr float kPxMove = 64.0f;            // m_O moves once a score passes it by 2^64
 constexpr float kPxMaxMove = 65536.0f;
 
@@ -125,12 +125,11 @@ static_assert(PxSmem::kBytes <= 227 * 1024, "shared memory budget");
 
 constexpr uint32_t kPxTmemCols = 512;
 // S 3 x 64, D (V as the tensor core expands it) 64, O 144, P 3 x 32, scales: all 512.
-constexpr uint32_t kPxColD = 192, kPxColO = 256, kPxColSfQ = 496, kPxColSfK = 500, kPxColSfV = 504, kPxColOne = 508;
-__device__ __forceinline__ uint32_t px_col_s(int set) { return 64u * set; }
-__device__ __forceinline__ uint32_t px_col_p(int set) { return 400u + 32u * set; }
+constexpr uint32_t kPxColS = 0, kPxColD = 128, kPxColO = 192, kPxColSfQ = 464, kPxColSfK = 468, kPxColSfV = 472, kPxColOne = 476;
+__device__ __forceinline__ uint32_t px_col_p(int set) { return 336u + 64u * set; }
 
 // Block-scaled E2M1 x E2M1, N = 64 keys; block-scaled E4M3 x E4M3, N = 32; bf16 x bf16, N = 144.
-constexpr uint32_t kPxIdQK = (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+constexpr uint32_t kPxIdQK = (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
 constexpr uint32_t kPxIdD = ((32u >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
 constexpr uint32_t kPxIdPV =
     (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t(PxSmem::kVRows) >> 3) << 17) | ((128u >> 4) << 24);
@@ -519,7 +518,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         init(S::kRawEmpty, kPxVStages, 1);
         init(S::kDFull, 2, 1);
         init(S::kDFree, 2, 4);
-        init(S::kVFull, kPxVSlots, 4);
+        init(S::kVFull, kPxVSlots, 8);
         init(S::kVEmpty, kPxVSlots, 1);
         init(S::kQFull, 2, 32);
         init(S::kQEmpty, 2, 1);
@@ -532,7 +531,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         init(S::kDrain, 1, 3);
         init(S::kUnitFull, kPxUnits, 1);
         // The three issuers, the expanding and the softmax warps.
-        init(S::kUnitEmpty, kPxUnits, 3 + 4 + kPxSoftmaxWarps);
+        init(S::kUnitEmpty, kPxUnits, 3 + 8 + kPxSoftmaxWarps);
         // A status already set by another launch or CTA: unwind at once, uniformly.
         *reinterpret_cast<uint32_t *>(smem + S::kMisc + 8) = 0;  // no tile to clear
         *abort_flag = (p.status && *reinterpret_cast<const volatile int32_t *>(p.status) != 0) ? 1u : 0u;
@@ -554,14 +553,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // (E4M3 1.0 is 0x38) and the scales of 2^0.
         const int tid = threadIdx.x - 32 * kPxExpandWarp;
 #pragma unroll 1
-        for (int i = tid; i < kPxVSlots * 16 * 8; i += 128) {
+        for (int i = tid; i < kPxVSlots * 16 * 8; i += 256) {
             const int slot = i >> 7, r = (i >> 3) & 15;
             const uint32_t v = r == 0 ? 0x3F803F80u : 0u;
             *reinterpret_cast<uint4 *>(smem + S::kV + slot * S::kVHalf + (128 + r) * 128 + (i & 7) * 16) =
                 make_uint4(v, v, v, v);
         }
 #pragma unroll 1
-        for (int i = tid; i < 32 * 8; i += 128) {
+        for (int i = tid; i < 32 * 8; i += 256) {
             const int r = i >> 3, at = (i & 7) ^ (r & 7);  // row r's 16-byte chunk `at`
             uint32_t w[4] = {0u, 0u, 0u, 0u};
             if (at == r >> 4) w[(r >> 2) & 3] = 0x38u << (8 * (r & 3));
@@ -584,12 +583,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     auto unit_done = [&](int c) { px_arrive(sb + S::kUnitEmpty + 8 * (c & (kPxUnits - 1))); };
 
     if (warp < kPxSoftmaxWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // ------------------------------------------------------------------ softmax
         const int quarter = warp & 3, set = warp >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t tS = tmem + lane_base + px_col_s(set);
+        const uint32_t tS = tmem + lane_base + kPxColS;
         const uint32_t a_ref = smem_u32(smem + S::kRef) + row * 8;
         const float sc = p.scale_log2;
         int k = 0;        // subtiles of this set so far
@@ -601,7 +600,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             ok = __all_sync(0xffffffffu, unit_wait(c));
             const PxUnit &u = *unit_at(c);
             if (!ok || u.T == 0) break;
-            const int n = 2 * u.T;
+            const int n = u.T;
             const int late = p.nq - 1 - (u.row0 + row - px_div(u.row0 + row, p.nq, p.m_nq) * p.nq);  // own keys after this row's token
             float m = -INFINITY;  // m_O as of this warp's last subtile; -inf: no key yet
             int i = first;
@@ -611,19 +610,19 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 // the subtile's end: a vote after each was a tenth of the loop.)
                 ok = wait(S::kSFull + 8 * set, k & 1);
                 tc_fence_after();
-                const PxTile tile = *tile_at(gt + (i >> 1));
+                const PxTile tile = *tile_at(gt + i);
                 const int lo = tile.rows & 0xFF, hi = (tile.rows >> 8) & 0xFF;
                 const bool active = lo < quarter * 32 + 32 && hi > quarter * 32;  // a row of the warp sees it
-                uint32_t s[2][32];
+                uint32_t s[4][32];
                 // Keys j < jv of the subtile are seen; a row of another sequence sees none.
                 const bool mine = row >= lo && row < hi;
-                int jv = tile.keys - 64 * (i & 1);
+                int jv = tile.keys;
                 if (p.causal && (tile.rows >> 16)) jv -= late;
-                if (__builtin_expect(active && __any_sync(0xffffffffu, mine && jv < 64), 0)) {
+                if (__builtin_expect(active && __any_sync(0xffffffffu, mine && jv < 128), 0)) {
                     // Masked in place, in a short loop: unrolled over the registers it took 2.7 KB
                     // of the instruction cache that all roles share.
 #pragma unroll 1
-                    for (int j0 = 0; j0 < 64; j0 += 16) {
+                    for (int j0 = 0; j0 < 128; j0 += 16) {
                         uint32_t v[16];
                         tc_ld_32x32b_x16(tS + j0, v);
                         tc_wait_ld16(v);
@@ -635,23 +634,23 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     tc_wait_st();
                 }
                 if (active) {
-                    tc_ld_32x32b_x32(tS, s[0]);
-                    tc_ld_32x32b_x32(tS + 32, s[1]);
-                    tc_wait_ld32(s[0]);
-                    tc_wait_ld32(s[1]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc_ld_32x32b_x32(tS + 32 * q, s[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc_wait_ld32(s[q]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) px_arrive(sb + S::kSFree + 8 * set);  // the next S of this set, while P is computed
                 float hm = -INFINITY;
                 if (active) {
-                    hm = sc * fmaxf(max32(s[0]), max32(s[1]));
+                    hm = sc * fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
                     if (!mine) hm = -INFINITY;
                 }
                 // The reference, after the last subtile's owner.
                 int E = 0;
                 const int ps = set == 0 ? kPxSets - 1 : set - 1;
-                const int seqno = 2 * gt + i;  // the subtile's number in the share
+                const int seqno = gt + i;  // the subtile's number in the share
                 if (i > 0) ok &= px_take(a_ref, seqno - 1, flag, m);
                 if (i == 0 || (hm > m && (m == -INFINITY || hm - m > kPxMove))) {
                     if (m > -INFINITY) {
@@ -677,15 +676,15 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 tc_fence_after();
                 if (!active) {
                     const uint32_t zero[16] = {};
-                    tc_st_32x32b_x16(tmem + lane_base + px_col_p(set), zero);
-                    tc_st_32x32b_x16(tmem + lane_base + px_col_p(set) + 16, zero);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc_st_32x32b_x16(tmem + lane_base + px_col_p(set) + 16 * q, zero);
                     tc_wait_st();
                 } else {
                     // p = 2^(s - m); 0 for a row that sees nothing here (hm = -inf).
                     const float nm = hm > -INFINITY ? -m : -INFINITY;
                     const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
+                    for (int q = 0; q < 4; ++q) {
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -918,8 +917,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // Each of the three products (S, P V, D) has an issuing thread of its own.
         if (elect_one()) {
             const uint32_t tSfQ = tmem + kPxColSfQ, tSfK = tmem + kPxColSfK;
-            int g = 0, set = 0;  // tiles, the next S buffer
-            uint32_t sph = 1;    // s_free's parity for it: free at first
+            int g = 0;  // tiles
             bool ok = true;
 #pragma unroll 1
             for (int c = 0; ok; ++c) {
@@ -942,22 +940,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     tc_fence_after();
                     px_cp_atom(tSfK, px_desc_lo(sb + S::kSfK, 0) + st * 32);
                     const uint32_t dK = px_desc_lo(sb + S::kK, 16) + st * (S::kKBytes >> 4);
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        ok = wait(S::kSFree + 8 * set, sph);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t tS = tmem + px_col_s(set), dKh = dK + half * (64 * 64 / 16);
-                        px_mma_mxf4<px_sf_id(kPxIdQK, 0)>(tS, dQ, dKh, tSfQ, tSfK + 2 * half, 0u);
-                        px_mma_mxf4<px_sf_id(kPxIdQK, 2)>(tS, dQ + 2, dKh + 2, tSfQ | (2u << 30),
-                                                          (tSfK + 2 * half) | (2u << 30), 1u);
-                        px_commit(sb + S::kSFull + 8 * set);
-                        if (++set == kPxSets) {
-                            set = 0;
-                            sph ^= 1;
-                        }
-                    }
+                    // The set of the tile before has read S.
+                    if (g > 0) ok = wait(S::kSFree + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1);
                     if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t tS = tmem + kPxColS;
+                    px_mma_mxf4<px_sf_id(kPxIdQK, 0)>(tS, dQ, dK, tSfQ, tSfK, 0u);
+                    px_mma_mxf4<px_sf_id(kPxIdQK, 2)>(tS, dQ + 2, dK + 2, tSfQ | (2u << 30), tSfK | (2u << 30), 1u);
+                    px_commit(sb + S::kSFull + 8 * (g & 1));
                     px_commit(sb + S::kKEmpty + 8 * st);
                 }
                 if (!ok) break;
@@ -973,33 +963,36 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // --------------------------------------------------------------- P V issuer
         if (elect_one()) {
             const uint32_t tO = tmem + kPxColO, dV0 = px_desc_lo(sb + S::kV, 16);
-            int k = 0, set = 0;  // subtiles, the next set
-            uint32_t pph = 0;
+            int g = 0;  // tiles
             bool ok = true;
 #pragma unroll 1
             for (int c = 0; ok; ++c) {
                 ok = unit_wait(c);
-                const int n = 2 * unit_at(c)->T;
-                if (!ok || n == 0) break;
+                const int T = unit_at(c)->T;
+                if (!ok || T == 0) break;
                 unit_done(c);
 #pragma unroll 1
-                for (int i = 0; i < n; ++i, ++k) {
-                    const int slot = k & (kPxVSlots - 1);
-                    ok = wait(S::kVFull + 8 * slot, (k / kPxVSlots) & 1);
-                    if (ok && i == 0 && c >= 1) ok = wait(S::kOFree, (c - 1) & 1);
-                    ok = ok && wait(S::kPFull + 8 * set, pph);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t dV = dV0 + slot * (S::kVHalf >> 4), tP = tmem + px_col_p(set);
-                    px_mma_bf16<true>(tO, tP, dV, i > 0 ? 1u : 0u);
+                for (int i = 0; i < T; ++i, ++g) {
+                    const int set = g & 1;
+                    if (i == 0 && c >= 1) ok = wait(S::kOFree, (c - 1) & 1);
+                    ok = ok && wait(S::kPFull + 8 * set, (g >> 1) & 1);
 #pragma unroll
-                    for (int q = 1; q < 4; ++q) px_mma_bf16<false>(tO, tP + 8 * q, dV + 2 * q, 1u);
-                    px_commit(sb + S::kPvDone + 8 * set);
-                    px_commit(sb + S::kVEmpty + 8 * slot);
-                    if (++set == kPxSets) {
-                        set = 0;
-                        pph ^= 1;
+                    for (int half = 0; half < 2; ++half) {  // 64 keys
+                        const int slot = (2 * g + half) & (kPxVSlots - 1);
+                        ok = ok && wait(S::kVFull + 8 * slot, ((2 * g + half) / kPxVSlots) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t dV = dV0 + slot * (S::kVHalf >> 4), tP = tmem + px_col_p(set) + 32 * half;
+                        if (half == 0)
+                            px_mma_bf16<true>(tO, tP, dV, i > 0 ? 1u : 0u);
+                        else
+                            px_mma_bf16<false>(tO, tP, dV, 1u);
+#pragma unroll
+                        for (int q = 1; q < 4; ++q) px_mma_bf16<false>(tO, tP + 8 * q, dV + 2 * q, 1u);
+                        px_commit(sb + S::kVEmpty + 8 * slot);
                     }
+                    if (!ok) break;
+                    px_commit(sb + S::kPvDone + 8 * set);
                 }
                 if (!ok) break;
                 px_commit(sb + S::kOFull);
@@ -1069,10 +1062,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // power of two has 4 significant bits) and into the swizzled K-major row that P V
         // reads: one conversion for two values. (By shifts and multiplies on the codes it
         // took 9 instructions for four, as many as all of the softmax.)
-        const int quarter = warp & 3, ch = quarter * 32 + lane;
-        const uint32_t tD = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kPxColD;
+        // Four warps take D's first half, four its second: with four for both, they were what
+        // P V waited for (1100 clk a subtile).
+        const int quarter = warp & 3, ch = quarter * 32 + lane, q = (warp - kPxExpandWarp) >> 2;
+        const uint32_t tD = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kPxColD + 32 * q;
+        const uint32_t full = S::kDFull + 8 * q, free = S::kDFree + 8 * q;
         int k = 0;
-        uint32_t f0 = 0;  // D's first half: the parity of what comes next
+        uint32_t f = 0;  // the parity of what comes next
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; ok; ++c) {
@@ -1084,56 +1080,56 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++k) {
                 const int slot = k & (kPxVSlots - 1);
-                ok = wait(S::kVEmpty + 8 * slot, ((k / kPxVSlots) & 1) ^ 1);
-                const uint32_t row = sb + S::kV + slot * S::kVHalf + ch * 128;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {  // while the tensor core expands the other half
-                    ok &= wait(S::kDFull + 8 * q, q == 0 ? f0 : k & 1);
-                    if (q == 0) {
-                        f0 ^= 1;
-                        if (__builtin_expect((k & 1) == 0 && lds32(sb + S::kMisc + 8) == (k >> 1) + 1u, 0)) {
-                            // This tile ends early. Codes past the last token may be anything (a NaN
-                            // would spread): zeros, in the thread's channel.
-                            const int sv = (k >> 1) & (kPxVStages - 1), jv = tile_at(k >> 1)->keys;
-                            uint8_t *codes = smem + S::kRaw + sv * S::kRawBytes + ch * 128;
+                ok = wait(full, f);
+                f ^= 1;
+                if (q == 0 && (k & 1) == 0 && lds32(sb + S::kMisc + 8) == (k >> 1) + 1u) {
+                    // This tile ends early, and D is not there yet. Codes past the last token may be
+                    // anything (a NaN would spread): zeros, in the thread's channel.
+                    const int sv = (k >> 1) & (kPxVStages - 1), jv = tile_at(k >> 1)->keys;
+                    uint8_t *codes = smem + S::kRaw + sv * S::kRawBytes + ch * 128;
 #pragma unroll 1
-                            for (int at = jv >> 4; at < 8; ++at) {
-                                uint8_t *chunk = codes + ((at ^ (ch & 7)) << 4);
-                                if (16 * at >= jv) {
-                                    *reinterpret_cast<uint4 *>(chunk) = make_uint4(0, 0, 0, 0);
-                                } else {
+                    for (int at = jv >> 4; at < 8; ++at) {
+                        uint8_t *chunk = codes + ((at ^ (ch & 7)) << 4);
+                        if (16 * at >= jv) {
+                            *reinterpret_cast<uint4 *>(chunk) = make_uint4(0, 0, 0, 0);
+                        } else {
 #pragma unroll 1
-                                    for (int e = jv - 16 * at; e < 16; ++e) chunk[e] = 0;
-                                }
-                            }
-                            uint8_t *sfv = smem + S::kSfV + sv * 512 + (ch & 31) * 16 + (ch >> 5) * 4;
-#pragma unroll 1
-                            for (int at = (jv + 31) >> 5; at < 4; ++at) sfv[at] = 0;
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) px_arrive(sb + S::kDFree);
-                            ok &= wait(S::kDFull, f0);
-                            f0 ^= 1;
+                            for (int e = jv - 16 * at; e < 16; ++e) chunk[e] = 0;
                         }
                     }
-                    tc_fence_after();
-                    uint32_t d[32];
-                    tc_ld_32x32b_x32(tD + 32 * q, d);
-                    tc_wait_ld32(d);
-                    tc_fence_before();
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) px_arrive(sb + S::kDFree + 8 * q);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = cvt_bf16x2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sts128(row + (((4 * q + e) ^ (ch & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    uint8_t *sfv = smem + S::kSfV + sv * 512 + (ch & 31) * 16 + (ch >> 5) * 4;
+#pragma unroll 1
+                    for (int at = (jv + 31) >> 5; at < 4; ++at) sfv[at] = 0;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) px_arrive(sb + free);
+                    ok &= wait(full, f);
+                    f ^= 1;
                 }
-                if (!ok) break;
-                fence_proxy_async_smem();
+                ok &= wait(S::kVEmpty + 8 * slot, ((k / kPxVSlots) & 1) ^ 1);
+                tc_fence_after();
                 __syncwarp();
+                const uint32_t row = sb + S::kV + slot * S::kVHalf + ch * 128;
+#pragma unroll
+                for (int e0 = 0; e0 < 2; ++e0) {  // 16 tokens
+                    uint32_t d[16];
+                    tc_ld_32x32b_x16(tD + 16 * e0, d);
+                    tc_wait_ld16(d);
+                    if (e0 == 1) {
+                        tc_fence_before();
+                        if (lane == 0) px_arrive(sb + free);
+                    }
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = cvt_bf16x2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        sts128(row + (((4 * q + 2 * e0 + e) ^ (ch & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2],
+                               w[4 * e + 3]);
+                }
+                fence_proxy_async_smem();
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 if (lane == 0) px_arrive(sb + S::kVFull + 8 * slot);
             }
         }
