@@ -26,28 +26,44 @@
 // needs no block scale (its exponent takes p up to 2^64 above the reference), and
 // goes to TMEM without a swizzled store: about 3 instructions a score, so the
 // exponentials themselves (16 a clock and SM: 1024 clk a tile of 128 x 128) become
-// the bound. V costs 2.5 instructions an element to expand, exactly (an E4M3 value
-// times a power of two has 4 significant bits), on warps of their own.
+// the bound. Rounding p to bf16 in numerator and denominator alike moves a row's
+// output by at most 2^-8 of the spread of the values it averages.
+// V is expanded by the tensor core: the E4M3 codes and their scales times a unit
+// matrix (kind::mxf8f6f4) give fp32 in TMEM, which eight warps take to bf16, exactly
+// (an E4M3 value times a power of two has 4 significant bits), and into shared
+// memory. By shifts and multiplies on the codes that took 9 instructions for four
+// values, as many as all of the softmax.
 //
-// Softmax: three sets of four warps take turns on subtiles of 64 keys, one row per
-// thread. A set reads its S whole and frees the buffer at once, so the next S comes
-// while P is computed, and P V is on nobody's path. (P in the front of its own S
-// buffer, two sets on tiles of 128 keys: 2190 clk a tile of 128 x 128. Four sets of
-// 64 keys that hold S in TMEM until P is done: 2600, with 24 warps in each other's
-// way.)
+// Softmax: two sets of four warps take turns on tiles of 128 keys, one row per
+// thread. A set reads its S whole (128 registers) and frees the buffer at once, so the
+// next tile's S comes while P is computed, and P V is on nobody's path. What a tile costs
+// beside its exponentials (waits, the reference, the store's end: some 1500 clk of short
+// dependent sequences) is paid once for 128 keys. (Three sets on 64 keys each: 286 us
+// where this takes 278, and the 64 registers saved bought nothing.)
 //
-// O has one reference per row, m_O, the row max of the unit's first subtile, and
+// O has one reference per row, m_O, the row max of the unit's first tile, and
 // p = 2^(s - m_O). It moves only when a score passes it by 2^64 (bf16 and fp32
 // keep their relative precision at any offset, so nothing is gained by moving it
-// sooner): the subtile's owner then scales its row of O after the P V before its own.
-// The reference passes from a subtile's owner to the next one's in shared memory,
+// sooner): the tile's owner then scales its row of O after the P V before its own.
+// The reference passes from a tile's owner to the next one's in shared memory,
 // right after the row max, well before the exponentials.
 // V carries a row of ones, so O column 128 sums P as rounded.
 //
-// Warp roles (640 threads): warps 0..11 softmax and epilogue, 12 feeder (units, queries,
-// key tiles), 13 TMEM allocator and issuer of S, 14 issuer of D, 15 issuer of P V, 16..19 V
-// expansion. The softmax warps hold 64 scores and need 128 registers, the others 48
-// (384 * 128 + 256 * 48 = the 640 * 96 of the launch).
+// Warp roles (640 threads): warps 0..7 softmax and epilogue, 8 feeder (units, queries,
+// key tiles), 9 TMEM allocator and issuer of S, 10 issuer of D, 11 issuer of P V, 12..19 V
+// expansion. The softmax warps hold 128 scores and get 168 registers, the others 48
+// (256 * 168 + 384 * 48 = the 640 * 96 of the launch).
+//
+// Measured (kernel, cold L2; the merge in brackets): 64 sequences of 64 query heads over 8 KV
+// heads with 8 query tokens, 16384 shared and up to 512 own keys: 278 us (12), 1.0 PFLOP/s;
+// 32 sequences of 32 heads, 8192 shared and up to 1024 own keys in pages: 30 us (4); 13 of
+// 20 heads with 3 tokens, 5003 and up to 777: 17 us (4); 4 of 32 heads, 1000 and up to 100:
+// 12 us (3.5). A tile takes 1.2 us in the long run, twice its exponentials. No one part is
+// the rest: without the exponentials the first case takes 264 us, without the expansion 273,
+// with half the P V 271, without any softmax work 239; the roles' loops are chains of dependent
+// instructions, each close to the tile's time. In the short cases 7 to 9 us are the start
+// (the schedule from the lengths, page numbers, the first loads) and 1.5 us the last unit's
+// partial results.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -95,7 +111,7 @@ struct PxSmem {
     static constexpr int kSfK = kSfQ + 2 * 512;
     static constexpr int kSfV = kSfK + kPxKStages * 512;
     static constexpr int kSfOne = kSfV + kPxVStages * 512;
-    static constexpr int kRef = kSfOne + 512;                     // (m_O, subtile) of each row
+    static constexpr int kRef = kSfOne + 512;                     // (m_O, tile) of each row
     static constexpr int kBar = kRef + 128 * 8;
     // Barriers (byte offsets).
     static constexpr int kKFull = kBar, kKEmpty = kKFull + 8 * kPxKStages;             // per stage
@@ -124,11 +140,11 @@ static_assert(PxSmem::kBar % 8 == 0 && PxSmem::kSfQ % 128 == 0, "alignment");
 static_assert(PxSmem::kBytes <= 227 * 1024, "shared memory budget");
 
 constexpr uint32_t kPxTmemCols = 512;
-// S 3 x 64, D (V as the tensor core expands it) 64, O 144, P 3 x 32, scales: all 512.
+// S 128, D (V as the tensor core expands it, 2 x 32 tokens) 64, O 144, P 2 x 64, scales 16: 480.
 constexpr uint32_t kPxColS = 0, kPxColD = 128, kPxColO = 192, kPxColSfQ = 464, kPxColSfK = 468, kPxColSfV = 472, kPxColOne = 476;
 __device__ __forceinline__ uint32_t px_col_p(int set) { return 336u + 64u * set; }
 
-// Block-scaled E2M1 x E2M1, N = 64 keys; block-scaled E4M3 x E4M3, N = 32; bf16 x bf16, N = 144.
+// Block-scaled E2M1 x E2M1, N = 128 keys; block-scaled E4M3 x E4M3, N = 32; bf16 x bf16, N = 144.
 constexpr uint32_t kPxIdQK = (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
 constexpr uint32_t kPxIdD = ((32u >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
 constexpr uint32_t kPxIdPV =
@@ -256,8 +272,8 @@ __device__ __forceinline__ bool px_wait(uint32_t bar, uint32_t parity, uint32_t 
     return ok != 0;
 }
 
-// The reference of a row goes from a subtile's owner to the next one's as one 8-byte word with
-// the subtile's number. px_take: false past 2^31 clocks or once the abort flag is up.
+// The reference of a row goes from a tile's owner to the next one's as one 8-byte word with the
+// tile's number. px_take: false past 2^31 clocks or once the abort flag is up.
 __device__ __forceinline__ void px_pass(uint32_t at, int seqno, float m) {
     asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(__float_as_uint(m)), "r"(seqno) : "memory");
 }
@@ -591,8 +607,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const uint32_t tS = tmem + lane_base + kPxColS;
         const uint32_t a_ref = smem_u32(smem + S::kRef) + row * 8;
         const float sc = p.scale_log2;
-        int k = 0;        // subtiles of this set so far
-        int first = set;  // how far this set's next subtile lies in its unit
+        int k = 0;        // tiles of this set so far
+        int first = set;  // how far this set's next tile lies in its unit
         int gt = 0;       // tiles of the units so far
         bool ok = true;
 #pragma unroll 1
@@ -602,19 +618,19 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             if (!ok || u.T == 0) break;
             const int n = u.T;
             const int late = p.nq - 1 - (u.row0 + row - px_div(u.row0 + row, p.nq, p.m_nq) * p.nq);  // own keys after this row's token
-            float m = -INFINITY;  // m_O as of this warp's last subtile; -inf: no key yet
+            float m = -INFINITY;  // m_O as of this warp's last tile; -inf: no key yet
             int i = first;
 #pragma unroll 1
             for (; i < n; i += kPxSets, ++k) {
                 // (A wait that gave up lets the warp go on with whatever is there, to one vote at
-                // the subtile's end: a vote after each was a tenth of the loop.)
+                // the tile's end: a vote after each was a tenth of the loop.)
                 ok = wait(S::kSFull + 8 * set, k & 1);
                 tc_fence_after();
                 const PxTile tile = *tile_at(gt + i);
                 const int lo = tile.rows & 0xFF, hi = (tile.rows >> 8) & 0xFF;
                 const bool active = lo < quarter * 32 + 32 && hi > quarter * 32;  // a row of the warp sees it
                 uint32_t s[4][32];
-                // Keys j < jv of the subtile are seen; a row of another sequence sees none.
+                // Keys j < jv of the tile are seen; a row of another sequence sees none.
                 const bool mine = row >= lo && row < hi;
                 int jv = tile.keys;
                 if (p.causal && (tile.rows >> 16)) jv -= late;
@@ -647,10 +663,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     hm = sc * fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
                     if (!mine) hm = -INFINITY;
                 }
-                // The reference, after the last subtile's owner.
+                // The reference, after the last tile's owner.
                 int E = 0;
                 const int ps = set == 0 ? kPxSets - 1 : set - 1;
-                const int seqno = gt + i;  // the subtile's number in the share
+                const int seqno = gt + i;  // the tile's number in the share
                 if (i > 0) ok &= px_take(a_ref, seqno - 1, flag, m);
                 if (i == 0 || (hm > m && (m == -INFINITY || hm - m > kPxMove))) {
                     if (m > -INFINITY) {
@@ -661,13 +677,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     }
                 }
                 px_pass(a_ref, seqno, m);
-                // This set's P is free once P V of its last subtile is done. A warp without rows
+                // This set's P is free once P V of its last tile is done. A warp without rows
                 // waits as well: else it could arrive at p_full a second time before the set's
                 // other warps have once.
                 ok &= wait(S::kPvDone + 8 * set, (k & 1) ^ 1);
                 if (i > 0 && __builtin_expect(__any_sync(0xffffffffu, E != 0), 0)) {
-                    // O holds the subtiles before this one: scale its rows before P V. (The phase
-                    // before the awaited one is complete: P V of this set's last subtile came
+                    // O holds the tiles before this one: scale its rows before P V. (The phase
+                    // before the awaited one is complete: P V of this set's last tile came
                     // after it.)
                     ok &= wait(S::kPvDone + 8 * ps, (set == 0 ? k - 1 : k) & 1);
                     tc_fence_after();
@@ -704,7 +720,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 if (!ok) break;
                 if (lane == 0) px_arrive(sb + S::kPFull + 8 * set);
             }
-            const bool owns_last = i == n + kPxSets - 1;  // this set had the unit's last subtile
+            const bool owns_last = i == n + kPxSets - 1;  // this set had the unit's last tile
             first = i - n;
             gt += u.T;
             if (!ok) break;
@@ -721,7 +737,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 // [slot][32 chunks of 4 channels][128 rows][4]: a warp stores its 32 rows side by side.
                 float4 *dst = reinterpret_cast<float4 *>(p.part_o) + slot * (32 * 128) + row;
 #pragma unroll 1
-                for (int q = set; q < 8; q += kPxSets) {  // 16 channels at a time: 3, 3 and 2 for the sets
+                for (int q = set; q < 8; q += kPxSets) {  // 16 channels at a time
                     uint32_t o[16];
                     tc_ld_32x32b_x16(tmem + lane_base + kPxColO + 16 * q, o);
                     tc_wait_ld16(o);
@@ -733,7 +749,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                                             __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
                     }
                 }
-                // The owner of the unit's last subtile has m_O of its end.
+                // The owner of the unit's last tile has m_O of its end.
                 if (owns_last && row < u.rows) p.part_lse[slot * 128 + row] = l > 0.f ? log2f(l) + m : -INFINITY;
                 if (threadIdx.x == 0) {
                     if (u.edge & 1) p.first[un] = static_cast<int>(blockIdx.x);
@@ -1058,12 +1074,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------------- V expansion
-        // A thread takes its channel's 64 values of D to bf16 (exact: an E4M3 value times a
-        // power of two has 4 significant bits) and into the swizzled K-major row that P V
-        // reads: one conversion for two values. (By shifts and multiplies on the codes it
-        // took 9 instructions for four, as many as all of the softmax.)
+        // A thread takes its channel's 32 values of D to bf16, one conversion for two, and into
+        // the swizzled K-major row that P V reads.
         // Four warps take D's first half, four its second: with four for both, they were what
-        // P V waited for (1100 clk a subtile).
+        // P V waited for (1100 clk for 64 tokens).
         const int quarter = warp & 3, ch = quarter * 32 + lane, q = (warp - kPxExpandWarp) >> 2;
         const uint32_t tD = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kPxColD + 32 * q;
         const uint32_t full = S::kDFull + 8 * q, free = S::kDFree + 8 * q;
