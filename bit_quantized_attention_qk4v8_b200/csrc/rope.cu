@@ -43,8 +43,6 @@ __global__ void __launch_bounds__(256, 3) quantize_qk_rope_kernel(const __grid_c
     if (a.seqlens) len = min(len, a.seqlens[b]);
     const bool live = t < len;  // else padding: zero codes and scales
     const int nrot = a.rope.rotary >> 4;
-    RopeTrig g;
-    rope_load<kAdjacent>(a.rope, b, t, a.start ? a.start[b] : 0, j, live, a.status, g);
     int k0, k1;
     rope_chunks(kAdjacent, nrot, j, k0, k1);
     const int nblk = a.cap / 128;
@@ -65,6 +63,8 @@ __global__ void __launch_bounds__(256, 3) quantize_qk_rope_kernel(const __grid_c
         r0 = *reinterpret_cast<const uint4 *>(x0);
         r1 = *reinterpret_cast<const uint4 *>(x0 + xsecond);
     }
+    RopeTrig g;  // (after the rows: the position and then the table's row are a trip to memory each)
+    rope_load<kAdjacent>(a.rope, b, t, a.start ? a.start[b] : 0, j, live, a.status, g);
     const bool store = t < a.row_len;
     // The trip count is the same for all lanes of the warp (its row helpers shuffle). Padding
     // stays zero on the way through: zero codes and scales.

@@ -93,11 +93,16 @@ __device__ __forceinline__ void rope_load(const RopeParams &r, int b, int t, int
 #pragma unroll
     for (int a = 0; a < 4; ++a)
         if (a < r.n_axes) pos[a] = rope_position(r, b, t, a, base, status);
+    // The axes of the lane's pairs, two bits each: one run of 8, or two of 4.
+    const uint32_t axes =
+        kAdjacent ? static_cast<uint32_t>(r.pair_axis[0] >> (8 * j)) << 24 >> 24 |
+                        static_cast<uint32_t>(r.pair_axis[1] >> (8 * j)) << 24 >> 16
+                  : static_cast<uint32_t>((j < 4 ? r.pair_axis[0] : r.pair_axis[1]) >> (16 * (j & 3)));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int pair = kAdjacent ? 4 * (j + 8 * (i >> 2)) + (i & 3) : 8 * j + i;
         if (pair < half) {
-            const int axis = static_cast<int>((r.pair_axis[pair >> 5] >> (2 * (pair & 31))) & 3);
+            const int axis = static_cast<int>((axes >> (2 * i)) & 3);
             const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
             const float2 v = *reinterpret_cast<const float2 *>(r.table + static_cast<int64_t>(at) * r.rotary + 2 * pair);
             if (i & 1) {
@@ -269,37 +274,47 @@ __device__ __forceinline__ void mxfp4_row8(const uint32_t (&w0)[4], const uint32
     }
     uint32_t e;  // exponent fields of the two chunks' largest magnitudes
     if (kHadamard) {
+        // Two values to an instruction from the second stage on: pairs (2i, 2i + 1).
+        float2 u0[4], u1[4];
 #pragma unroll
-        for (int s = 1; s < 8; s *= 2) {
+        for (int i = 0; i < 4; ++i) {
+            u0[i] = make_float2(v0[2 * i] + v0[2 * i + 1], v0[2 * i] - v0[2 * i + 1]);
+            u1[i] = make_float2(v1[2 * i] + v1[2 * i + 1], v1[2 * i] - v1[2 * i + 1]);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+        for (int s = 1; s < 4; s *= 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 if (i & s) continue;
-                const float a = v0[i], b = v0[i + s];
-                v0[i] = a + b;
-                v0[i + s] = a - b;
-                const float c = v1[i], d = v1[i + s];
-                v1[i] = c + d;
-                v1[i + s] = c - d;
+                const float2 a = u0[i], b = u0[i + s], c = u1[i], d = u1[i + s];
+                u0[i] = fadd2(a, b);
+                u0[i + s] = fsub2(a, b);
+                u1[i] = fadd2(c, d);
+                u1[i + s] = fsub2(c, d);
             }
         }
 #pragma unroll
         for (int m = 1; m < 8; m *= 2) {  // strides 8, 16, 32: the row's other lanes
             const float sgn = (j & m) != 0 ? -1.f : 1.f;  // fma(+-1, v, o) rounds as o - v, v + o
+            const float2 sgn2 = make_float2(sgn, sgn);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v0[i] = fmaf(sgn, v0[i], __shfl_xor_sync(0xffffffffu, v0[i], m));
-                v1[i] = fmaf(sgn, v1[i], __shfl_xor_sync(0xffffffffu, v1[i], m));
+            for (int i = 0; i < 4; ++i) {
+                const float2 o0 = make_float2(__shfl_xor_sync(0xffffffffu, u0[i].x, m), __shfl_xor_sync(0xffffffffu, u0[i].y, m));
+                const float2 o1 = make_float2(__shfl_xor_sync(0xffffffffu, u1[i].x, m), __shfl_xor_sync(0xffffffffu, u1[i].y, m));
+                u0[i] = ffma2(sgn2, u0[i], o0);
+                u1[i] = ffma2(sgn2, u1[i], o1);
             }
         }
         constexpr float kRsqrt128 = 0x1.6a09e6p-4f;
+        const float2 r2 = make_float2(kRsqrt128, kRsqrt128);
         uint32_t m0 = 0, m1 = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {  // stride 64: the lane's two chunks
-            const float a = v0[i], b = v1[i];
-            v0[i] = (a + b) * kRsqrt128;
-            v1[i] = (a - b) * kRsqrt128;
-            m0 = max(m0, __float_as_uint(v0[i]) & 0x7FFFFFFFu);
-            m1 = max(m1, __float_as_uint(v1[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 4; ++i) {  // stride 64: the lane's two chunks
+            const float2 a = fmul2(fadd2(u0[i], u1[i]), r2), b = fmul2(fsub2(u0[i], u1[i]), r2);
+            v0[2 * i] = a.x, v0[2 * i + 1] = a.y;
+            v1[2 * i] = b.x, v1[2 * i + 1] = b.y;
+            m0 = max(m0, max(__float_as_uint(a.x) & 0x7FFFFFFFu, __float_as_uint(a.y) & 0x7FFFFFFFu));
+            m1 = max(m1, max(__float_as_uint(b.x) & 0x7FFFFFFFu, __float_as_uint(b.y) & 0x7FFFFFFFu));
         }
         e = (m0 >> 23) | ((m1 >> 23) << 16);
     } else {
@@ -331,7 +346,11 @@ __device__ __forceinline__ void mxfp4_row8(const uint32_t (&w0)[4], const uint32
 
 // How a warp takes rows: TS tokens by HS heads at a time (TS * HS = 4), `heads` heads
 // (a multiple of HS) of its tokens in all, so that a token's cosines and sines
-// are read once for them.
+// are read once for them. With 32 heads or more, one token by four heads: 8 steps use its
+// cosines up, and the table is read once for 32 rows (96 us for 32768 tokens of 32
+// heads; four tokens by one head: 99). With fewer, four tokens by one head, so that a lane's
+// cosines still serve a head a step (8192 appended tokens of 8 heads, 4 sequences: 55 us;
+// one token by four heads: 64).
 struct RopeTiling {
     int hs_log2;        // HS = 1, 2 or 4
     int heads;          // heads of one item
@@ -341,7 +360,8 @@ struct RopeTiling {
 
 inline RopeTiling rope_tiling(int B, int tokens, int H) {
     RopeTiling t;
-    t.hs_log2 = H >= 3 ? 2 : H - 1;
+    t.hs_log2 = H >= 32 || tokens == 1 ? 2 : tokens == 2 ? 1 : 0;
+    if (H < 3) t.hs_log2 = H - 1 < t.hs_log2 ? H - 1 : t.hs_log2;
     const int hs = 1 << t.hs_log2, ts = 4 >> t.hs_log2;
     t.token_groups = (tokens + ts - 1) / ts;
     // Up to 8 steps over the heads an item, fewer while the items would not give
