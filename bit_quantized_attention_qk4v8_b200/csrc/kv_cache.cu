@@ -348,8 +348,6 @@ __device__ __forceinline__ void append_v_page(const KvAppendRopeArgs &a, int idx
     const int p0 = ((L0 >> 7) + pg) * 128;  // first token of the page
     if (p0 >= L1) return;
     const int lo = max(L0 & ~31, p0), hi = min((L1 + 31) & ~31, p0 + 128);  // touched groups' tokens
-    const int page = page_of(a.block_table, a.max_pages, a.num_pages, b, p0);
-    if (page < 0 && threadIdx.x == 0) flag_bad_page(a.status);
     uint16_t *tail = reinterpret_cast<uint16_t *>(a.tail) + static_cast<int64_t>(bh) * (32 * 128);
     const uint16_t *vin = reinterpret_cast<const uint16_t *>(a.v) + b * a.vsb + h * a.vsh;
     uint4 raw[8];
@@ -365,6 +363,8 @@ __device__ __forceinline__ void append_v_page(const KvAppendRopeArgs &a, int idx
                 raw[k] = *reinterpret_cast<const uint4 *>(vin + static_cast<int64_t>(t - L0) * a.vst + ch);
         }
     }
+    const int page = page_of(a.block_table, a.max_pages, a.num_pages, b, p0);  // during the loads
+    if (page < 0 && threadIdx.x == 0) flag_bad_page(a.status);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int i = threadIdx.x + 256 * k;
