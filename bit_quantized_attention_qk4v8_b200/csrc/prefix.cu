@@ -39,7 +39,7 @@
 // next tile's S comes while P is computed, and P V is on nobody's path. What a tile costs
 // beside its exponentials (waits, the reference, the store's end: some 1500 clk of short
 // dependent sequences) is paid once for 128 keys. (Three sets on 64 keys each: 286 us
-// where this takes 278, and the 64 registers saved bought nothing.)
+// where this took 278, and the 64 registers saved bought nothing.)
 //
 // O has one reference per row, m_O, the row max of the unit's first tile, and
 // p = 2^(s - m_O). It moves only when a score passes it by 2^64 (bf16 and fp32
@@ -49,18 +49,22 @@
 // right after the row max, well before the exponentials.
 // V carries a row of ones, so O column 128 sums P as rounded.
 //
+// Rows of several sequences share the tiles of own keys, so what one sequence's keys
+// and values hold must not reach the others' rows, which take them with weight 0: their scores
+// stay finite (kPxQShift), and V goes into bf16 without infinities and NaN. 5 us of the 283.
+//
 // Warp roles (640 threads): warps 0..7 softmax and epilogue, 8 feeder (units, queries,
 // key tiles), 9 TMEM allocator and issuer of S, 10 issuer of D, 11 issuer of P V, 12..19 V
 // expansion. The softmax warps hold 128 scores and get 168 registers, the others 48
 // (256 * 168 + 384 * 48 = the 640 * 96 of the launch).
 //
 // Measured (kernel, cold L2; the merge in brackets): 64 sequences of 64 query heads over 8 KV
-// heads with 8 query tokens, 16384 shared and up to 512 own keys: 278 us (12), 1.0 PFLOP/s;
+// heads with 8 query tokens, 16384 shared and up to 512 own keys: 283 us (12), 0.99 PFLOP/s;
 // 32 sequences of 32 heads, 8192 shared and up to 1024 own keys in pages: 30 us (4); 13 of
 // 20 heads with 3 tokens, 5003 and up to 777: 17 us (4); 4 of 32 heads, 1000 and up to 100:
 // 12 us (3.5). A tile takes 1.2 us in the long run, twice its exponentials. No one part is
-// the rest: without the exponentials the first case takes 264 us, without the expansion 273,
-// with half the P V 271, without any softmax work 239; the roles' loops are chains of dependent
+// the rest: of 278 us (before V's and the scores' guards), 264 are left without the exponentials,
+// 273 without the expansion, 271 with a quarter of P V, 239 without any softmax work; the roles' loops are chains of dependent
 // instructions, each close to the tile's time. In the short cases 7 to 9 us are the start
 // (the schedule from the lengths, page numbers, the first loads) and 1.5 us the last unit's
 // partial results.
@@ -95,6 +99,13 @@ constexpr int kPxExpandWarp = kPxSoftmaxWarps + 4;
 constexpr int kPxThreads = 32 * (kPxExpandWarp + 8);
 constexpr float kPxMove = 64.0f;            // m_O moves once a score passes it by 2^64
 constexpr float kPxMaxMove = 65536.0f;
+// The queries' scales are taken 2^-64 smaller (the softmax scale is 2^64 larger): so the scores that
+// a row gets from other sequences' keys, which share its tile, stay finite even where those hold what
+// the quantizer makes of an infinity or a NaN (6 * 2^126), and fma(s, scale, -inf) is -inf.
+// (Scales of queries below 2^-63 count as 2^-63: scores of 2^-60 of the keys. Zeroing P of those
+// rows instead: 297 us where this takes 283.)
+constexpr uint32_t kPxQShift = 0x40404040u;
+constexpr float kPxQScale = 18446744073709551616.0f;  // 2^64
 
 struct PxSmem {
     static constexpr int kQBytes = 128 * 64;
@@ -205,6 +216,16 @@ __device__ __forceinline__ void px_arrive(uint32_t bar) {
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Two values of V in bf16, infinities and NaN as the largest finite values: the rows of other
+// sequences take it with weight 0, and 0 times it has to be 0.
+__device__ __forceinline__ uint32_t px_v_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("{\n\t.reg .b32 t;\n\tcvt.rn.satfinite.bf16x2.f32 t, %1, %2;\n\tmax.bf16x2 %0, t, %3;\n\t}"
+        : "=r"(d)
+        : "f"(hi), "f"(lo), "r"(0xFF7FFF7Fu));
     return d;
 }
 
@@ -606,7 +627,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_base + kPxColS;
         const uint32_t a_ref = smem_u32(smem + S::kRef) + row * 8;
-        const float sc = p.scale_log2;
+        const float sc = p.scale_log2 * kPxQScale;
         int k = 0;        // tiles of this set so far
         int first = set;  // how far this set's next tile lies in its unit
         int gt = 0;       // tiles of the units so far
@@ -686,9 +707,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     // before the awaited one is complete: P V of this set's last tile came
                     // after it.)
                     ok &= wait(S::kPvDone + 8 * ps, (set == 0 ? k - 1 : k) & 1);
+                    __syncwarp();
                     tc_fence_after();
                     px_rescale(tmem + lane_base + kPxColO, E);
                 }
+                __syncwarp();
                 tc_fence_after();
                 if (!active) {
                     const uint32_t zero[16] = {};
@@ -696,7 +719,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     for (int q = 0; q < 4; ++q) tc_st_32x32b_x16(tmem + lane_base + px_col_p(set) + 16 * q, zero);
                     tc_wait_st();
                 } else {
-                    // p = 2^(s - m); 0 for a row that sees nothing here (hm = -inf).
+                    // p = 2^(s - m); 0 for a row that sees nothing here (hm = -inf), whose scores are
+                    // finite whatever the keys (kPxQShift).
                     const float nm = hm > -INFINITY ? -m : -INFINITY;
                     const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
 #pragma unroll
@@ -931,46 +955,55 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     } else if (warp == kPxQkWarp) {
         // ------------------------------------------------------------- Q K^T issuer
         // Each of the three products (S, P V, D) has an issuing thread of its own.
-        if (elect_one()) {
-            const uint32_t tSfQ = tmem + kPxColSfQ, tSfK = tmem + kPxColSfK;
-            int g = 0;  // tiles
-            bool ok = true;
+        const uint32_t tSfQ = tmem + kPxColSfQ, tSfK = tmem + kPxColSfK, tS = tmem + kPxColS;
+        int g = 0;  // tiles
+        bool ok = true;
 #pragma unroll 1
-            for (int c = 0; ok; ++c) {
-                const int qb = c & 1;
-                ok = unit_wait(c);
-                const int T = unit_at(c)->T;
-                if (!ok || T == 0) break;
+        for (int c = 0; ok; ++c) {
+            const int qb = c & 1;
+            ok = __all_sync(0xffffffffu, unit_wait(c));
+            const int T = unit_at(c)->T;
+            if (!ok || T == 0) break;
+            ok = wait_warp(S::kQFull + 8 * qb, (c >> 1) & 1);
+            if (!ok) break;
+            {
+                uint4 *sf = reinterpret_cast<uint4 *>(smem + S::kSfQ + qb * 512) + lane;
+                uint4 v = *sf;
+                v.x = __vsubus4(v.x, kPxQShift), v.y = __vsubus4(v.y, kPxQShift);
+                v.z = __vsubus4(v.z, kPxQShift), v.w = __vsubus4(v.w, kPxQShift);
+                *sf = v;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one()) {
                 unit_done(c);
-                ok = wait(S::kQFull + 8 * qb, (c >> 1) & 1);
-                if (!ok) break;
-                fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t dQ = px_desc_lo(sb + S::kQ + qb * S::kQBytes, 16);
                 px_cp_atom(tSfQ, px_desc_lo(sb + S::kSfQ + qb * 512, 0));
 #pragma unroll 1
-                for (int i = 0; i < T; ++i, ++g) {
-                    const int st = g & (kPxKStages - 1);
-                    ok = wait(S::kKFull + 8 * st, (g / kPxKStages) & 1);
+                for (int j = g; j < g + T; ++j) {
+                    const int st = j & (kPxKStages - 1);
+                    ok = wait(S::kKFull + 8 * st, (j / kPxKStages) & 1);
+                    // The set of the tile before has read S.
+                    if (j > 0) ok &= wait(S::kSFree + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     px_cp_atom(tSfK, px_desc_lo(sb + S::kSfK, 0) + st * 32);
                     const uint32_t dK = px_desc_lo(sb + S::kK, 16) + st * (S::kKBytes >> 4);
-                    // The set of the tile before has read S.
-                    if (g > 0) ok = wait(S::kSFree + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t tS = tmem + kPxColS;
                     px_mma_mxf4<px_sf_id(kPxIdQK, 0)>(tS, dQ, dK, tSfQ, tSfK, 0u);
                     px_mma_mxf4<px_sf_id(kPxIdQK, 2)>(tS, dQ + 2, dK + 2, tSfQ | (2u << 30), tSfK | (2u << 30), 1u);
-                    px_commit(sb + S::kSFull + 8 * (g & 1));
+                    px_commit(sb + S::kSFull + 8 * (j & 1));
                     px_commit(sb + S::kKEmpty + 8 * st);
                 }
-                if (!ok) break;
-                px_commit(sb + S::kQEmpty + 8 * qb);
+                if (ok) px_commit(sb + S::kQEmpty + 8 * qb);
             }
+            g += T;
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (elect_one()) {
             if (!ok) px_give_up(abort_flag, p.status);
-            // Every tcgen05 operation of the issuers has completed once `drain` does.
+            // Every tcgen05 operation of the issuers has completed once `drain` does. (Of this warp
+            // the elected thread issues them all.)
             px_commit(sb + S::kDrain);
         }
         __syncwarp();
@@ -1135,7 +1168,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     }
                     uint32_t w[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = cvt_bf16x2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = px_v_bf16x2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         sts128(row + (((4 * q + 2 * e0 + e) ^ (ch & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2],

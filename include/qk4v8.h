@@ -501,7 +501,9 @@ QK4V8_API int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, 
  *   workspace  qk4v8_decode_prefix_workspace_bytes of the same sizes, 16-byte aligned.
  *            Calls that may overlap on the GPU need one each.
  *   out, lse, softmax_scale, dev_status and errors as for qk4v8_attention_decode. A
- *            row with no key at all outputs 0 with lse = -inf.
+ *            row with no key at all outputs 0 with lse = -inf. Sequences share tiles, not
+ *            results: where one's own keys or values come from infinities or NaN, its
+ *            rows are undefined and the others' are not touched.
  * Needs (Hq / Hkv) * nq <= 128. Two launches: the attention kernel over the prefix and
  * the own keys, and the merge of its partial results.
  *

@@ -168,6 +168,31 @@ def test_nothing_behind_the_last_token_is_seen(paged):
     assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
 
 
+@pytest.mark.parametrize("where", ["k", "v", "v_scale", "k_scale"])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_one_sequence_does_not_reach_another(where, bad):
+    """NaN or infinity in sequence 2's own keys or values: the others' bits stay, though their rows share its tiles.
+    (Key scales are the quantizer's, whose largest is 2^126, byte 0xFD; a value scale may be anything.)"""
+    lens, nq = [70, 200, 130, 5, 64, 129], 2
+    p = Problem(6, 8, 2, nq, 260, lens, seed=31)
+    clean = p.run()
+    if where in ("k", "v"):
+        x = (p.k if where == "k" else p.v).copy()
+        x[2, 100] = 0x7FC0 if bad == "nan" else 0x7F80
+        x[2, 129, :, ::3] = 0xFF80
+        d = to_dev(x)
+        if where == "k":
+            p.kp = qk.quantize_qk(d, cap=p.cap, seqlens=p.sl)
+        else:
+            p.vp = qk.quantize_v(d, cap=p.cap, seqlens=p.sl)
+    else:
+        t = (p.kp if where == "k_scale" else p.vp).scales
+        t[2, :, 0, :] = 0xFD if where == "k_scale" else 0xFF if bad == "nan" else 0xFE
+    out, lse = p.run()
+    others = [b for b in range(6) if b != 2]
+    assert torch.equal(out[others], clean[0][others]) and torch.equal(lse[others], clean[1][others])
+
+
 def test_bounds_that_are_loose_or_cut():
     p = Problem(4, 8, 2, 1, 200, [5, 100, 0, 161], cap=1024)
     check(p.run(max_seqlen=1024), p.reference())
