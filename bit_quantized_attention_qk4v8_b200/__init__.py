@@ -661,9 +661,18 @@ def _prefix_buffers(q: MXFP4, Hkv: int, prefix_len: int, max_seqlen: int, worksp
     if workspace is None:
         need = decode_prefix_workspace_bytes(q.B, q.H, Hkv, q.length, prefix_len, max_seqlen)
         workspace = torch.empty((max(16, need),), dtype=torch.uint8, device=dev)
+    else:
+        _check_dense(dev, workspace)
     if out is None:
         out = torch.empty((q.B, q.length, q.H, D), dtype=torch.bfloat16, device=dev)
-    if return_lse and lse is None:
+    elif out.dtype != torch.bfloat16 or out.device != dev or tuple(out.shape) != (q.B, q.length, q.H, D) or \
+            not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 tensor [B, nq, Hq, 128] on q's device")
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (q.B, q.H, q.length) or \
+                not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous float32 tensor [B, Hq, nq] on q's device")
+    elif return_lse:
         lse = torch.empty((q.B, q.H, q.length), dtype=torch.float32, device=dev)
     return workspace, workspace.numel() * workspace.element_size(), out, lse
 

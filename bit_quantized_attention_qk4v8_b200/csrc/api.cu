@@ -1153,7 +1153,8 @@ int plan_prefix(int B, int Hq, int Hkv, int nq, int prefix_len, int max_seqlen, 
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || nq < 1 || nq > 8 || (Hq / Hkv) * nq > 128)
         return set_error(QK4V8_ERR_INVALID_ARG, "need 1 <= nq <= 8 and (Hq/Hkv)*nq <= 128 (B=%d Hq=%d Hkv=%d nq=%d)", B,
                          Hq, Hkv, nq);
-    if (prefix_len < 0 || max_seqlen < 0)
+    // (Rounded up to tiles they have to stay an int.)
+    if (prefix_len < 0 || max_seqlen < 0 || prefix_len > 0x7FFFFF80 || max_seqlen > 0x7FFFFF80)
         return set_error(QK4V8_ERR_INVALID_ARG, "bad lengths prefix_len=%d max_seqlen=%d", prefix_len, max_seqlen);
     int sms = 148, dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||

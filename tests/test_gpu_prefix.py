@@ -224,6 +224,11 @@ def test_buffers_of_the_caller():
     assert torch.equal(only, out)
     with pytest.raises(qk.QK4V8Error):
         p.run(workspace=guard[:need - 16])
+    for bad in (dict(out=out.float()), dict(out=out[:, :1]), dict(out=out.cpu()), dict(out=out.transpose(1, 2)),
+                dict(lse=lse.half()), dict(lse=lse[:2]), dict(lse=lse.cpu()), dict(workspace=guard.cpu()),
+                dict(workspace=guard[::2])):
+        with pytest.raises(ValueError):
+            p.run(**bad)
     for bad in (dict(k=p.pkp), dict(v=p.kp), dict(pk=p.kp), dict(v=qk.MXFP8V(p.vp.codes[..., ::2], p.vp.scales, 4, 2, p.vp.cap, 1))):
         a = dict(pk=p.pkp, pv=p.pvp, k=p.kp, v=p.vp)
         a.update(bad)

@@ -107,7 +107,7 @@ def paged(lib, **kw):
 
 @pytest.mark.parametrize("kw", [
     dict(ptab=None), dict(table=None), dict(max_pages=0), dict(max_pages=1 << 24), dict(pages=0), dict(pages=1 << 30),
-    dict(most=513), dict(lens=None), dict(Hkv=0), dict(wsb=0)])
+    dict(most=513), dict(lens=None), dict(Hkv=0), dict(wsb=0), dict(plen=2**31 - 1)])
 def test_paged_prefix_refuses(lib, kw):
     assert paged(lib, **kw) == INVALID
 
