@@ -619,6 +619,24 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     auto unit_wait = [&](int c) { return wait(S::kUnitFull + 8 * (c & (kPxUnits - 1)), (c / kPxUnits) & 1); };
     auto unit_done = [&](int c) { px_arrive(sb + S::kUnitEmpty + 8 * (c & (kPxUnits - 1))); };
 
+    // Rows r0 .. r1 - 1 of a unit's queries into buffer qb by the warp, four lanes to a row: copies
+    // that need no register, all in flight (a spilled register goes to L2, as shared memory leaves
+    // next to no L1: the gather by loads took 12 us a unit). Rows past the unit's are zero.
+    auto gather = [&](const PxUnit &u, int qb, int r0, int r1) {
+        const int chunk = lane & 3;
+#pragma unroll 1
+        for (int r = r0 + (lane >> 2); r < r1; r += 8) {
+            const bool any = r < u.rows;
+            int t = 0;
+            const int64_t bh = any ? px_row(p, u.h, u.row0 + r, t) : 0;
+            px_copy16(sb + S::kQ + qb * S::kQBytes + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4),
+                      p.q_codes + (bh * p.q_cap + t) * 64 + chunk * 16, any);
+            if (chunk == 0)
+                px_copy4(sb + S::kSfQ + qb * 512 + (r & 31) * 16 + (r >> 5) * 4,
+                         p.q_scales + bh * (p.q_cap / 128) * 512 + t * 16, any);
+        }
+    };
+
     if (warp < kPxSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // ------------------------------------------------------------------ softmax
@@ -792,8 +810,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kPxFeedWarp) {
         // --------------------------------------------------------------------- feeder
-        // Announces the units, two ahead, gathers each one's query rows (the warp) and loads
-        // its key tiles. A unit's rows come before its keys, so they are there when the unit
+        // Announces the units, gathers each one's query rows (the warp) and loads its key
+        // tiles. A unit's rows come before its keys, so they are there when the unit
         // before ends.
         int announced = 0;
         auto announce = [&]() -> bool {
@@ -897,40 +915,18 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll 1
         for (int c = 0; ok; ++c) {
 #pragma unroll 1
-            while (ok && announced < c + 2) ok = announce();
+            while (ok && announced <= c) ok = announce();
             const PxUnit &u = *unit_at(c);
             if (!ok || u.T == 0) break;
             const int qb = c & 1;
             ok = wait_warp(S::kQEmpty + 8 * qb, ((c >> 1) & 1) ^ 1);
             if (!ok) break;
-            uint8_t *qbuf = smem + S::kQ + qb * S::kQBytes;
-            uint8_t *sfq = smem + S::kSfQ + qb * 512;
-            // Copies that need no register, all in flight: this warp has few, and a spilled one
-            // goes to L2 (shared memory leaves next to no L1). Lane l finds rows l + 32 j and
-            // copies their scales; then 16-byte chunk l % 4 of rows l / 4 + 8 i. Rows past the
-            // unit's are zero.
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                const int r = lane + 32 * j;
-                int64_t at = -1;  // the row of 64 bytes of codes
-                int64_t sf = 0;
-                if (r < u.rows) {
-                    int t;
-                    const int64_t bh = px_row(p, u.h, u.row0 + r, t);
-                    at = bh * p.q_cap + t;
-                    sf = bh * (p.q_cap / 128) * 512 + t * 16;
-                }
-                px_copy4(smem_u32(sfq + lane * 16 + j * 4), p.q_scales + sf, at >= 0);
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int rr = 32 * j + (lane >> 2) + 8 * i;
-                    const int64_t a = __shfl_sync(0xffffffffu, at, (lane >> 2) + 8 * i);
-                    px_copy16(smem_u32(qbuf + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4)),
-                              p.q_codes + (a > 0 ? a : 0) * 64 + (lane & 3) * 16, a >= 0);
-                }
-            }
             // q_full completes with the copies; its waiter makes them visible to the tensor core.
-            if (!(p.test_stall && c == 0)) px_arrive_copies(sb + S::kQFull + 8 * qb);
+            // The first unit's rows are the expanding warps', which wait for V then.
+            if (c > 0) {
+                gather(u, qb, 0, 128);
+                px_arrive_copies(sb + S::kQFull + 8 * qb);
+            }
             seek(u);
             ok = load(u, u.T);
         }
@@ -1122,6 +1118,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             ok = __all_sync(0xffffffffu, unit_wait(c));
             const int n = 2 * unit_at(c)->T;
             if (!ok || n == 0) break;
+            if (c == 0) {  // the first unit's queries, 16 rows a warp
+                const int r0 = 16 * (warp - kPxExpandWarp);
+                gather(*unit_at(0), 0, r0, r0 + 16);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                if (lane < 4 && !p.test_stall) px_arrive(sb + S::kQFull);  // 32 in all, as from the feeder
+            }
             __syncwarp();
             if (lane == 0) unit_done(c);
 #pragma unroll 1
