@@ -62,10 +62,10 @@
 // heads with 8 query tokens, 16384 shared and up to 512 own keys: 283 us (12), 0.99 PFLOP/s;
 // 32 sequences of 32 heads, 8192 shared and up to 1024 own keys in pages: 30 us (4); 13 of
 // 20 heads with 3 tokens, 5003 and up to 777: 17 us (4); 4 of 32 heads, 1000 and up to 100:
-// 12 us (3.5). A tile takes 1.2 us in the long run, twice its exponentials. No one part is
+// 11 us (3.5). A tile takes 1.2 us in the long run, twice its exponentials. No one part is
 // the rest: of 278 us (before V's and the scores' guards), 264 are left without the exponentials,
 // 273 without the expansion, 271 with a quarter of P V, 239 without any softmax work; the roles' loops are chains of dependent
-// instructions, each close to the tile's time. In the short cases 7 to 9 us are the start
+// instructions, each close to the tile's time. In the short cases 6 to 8 us are the start
 // (the schedule from the lengths, page numbers, the first loads) and 1.5 us the last unit's
 // partial results.
 #include <cuda_bf16.h>
