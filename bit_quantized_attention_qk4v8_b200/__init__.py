@@ -625,11 +625,13 @@ def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rop
     cache.seqlens advances on the device, unless seqlens_out (int32 [B]) receives the new lengths."""
     _check_bf16(k_new, "k_new")
     _check_bf16(v_new, "v_new")
-    B, n_new, Hkv, _ = k_new.shape
-    dev = k_new.device
-    if v_new.shape != k_new.shape or v_new.device != dev:
+    shape, dev = k_new.shape, k_new.device
+    B, n_new, Hkv, _ = shape
+    if v_new.shape != shape or v_new.device != dev:
         raise ValueError("k_new and v_new must have the same shape and device")
-    if B != cache.B or Hkv != cache.Hkv:
+    num_pages, heads = cache.k_codes.shape[:2]
+    rows, max_pages = cache.block_table.shape
+    if B != rows or Hkv != heads:
         raise ValueError("k_new must be [cache.B, n_new, cache.Hkv, 128]")
     _check_dense(dev, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, cache.v_tail, cache.block_table,
                  cache.seqlens)
@@ -641,7 +643,7 @@ def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rop
     with _on(dev):
         check(lib().qk4v8_kv_append_rope(k_new.data_ptr(), v_new.data_ptr(), B, n_new, Hkv, D, ctypes.addressof(ks),
                                          ctypes.addressof(vs), lens, nl, so, ctypes.addressof(rs),
-                                         cache.block_table.data_ptr(), cache.max_pages, cache.num_pages,
+                                         cache.block_table.data_ptr(), max_pages, num_pages,
                                          cache.k_codes.data_ptr(), cache.k_scales.data_ptr(),
                                          cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), cache.v_tail.data_ptr(),
                                          int(cache.hadamard_k), _ptr(dev_status), _stream(dev)),

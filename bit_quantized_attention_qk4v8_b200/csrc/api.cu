@@ -1245,7 +1245,9 @@ int decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq
     }
     if (plan.own) {
         const int map_rows = paged ? pages.num_pages * Hkv : B * Hkv, map_cap = paged ? 128 : kv_cap;
-        if ((st = make_k_map(&k, k_codes, map_rows, map_cap)) || (st = make_v_map(&v, v_codes, map_rows, map_cap)))
+        if (paged && plan.tiles)  // one pool
+            k = pk, v = pv;
+        else if ((st = make_k_map(&k, k_codes, map_rows, map_cap)) || (st = make_v_map(&v, v_codes, map_rows, map_cap)))
             return st;
         p.own = 1;
         // Lengths past max_seqlen are cut to it: no read behind the cache or its block table.
