@@ -492,7 +492,7 @@ QK4V8_API int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, 
  * result is attention over both: the prefix is read once for 128 query rows
  * (128 / (G * nq) sequences) rather than once for each sequence.
  *   q_*      packed MXFP4 Q, [B][Hq][q_cap], nq (1..8) tokens (the rows past nq
- *            are not read by the prefix part)
+ *            are not read)
  *   p_k_*, p_v_*  packed MXFP4 K and MXFP8 V of the prefix, [1][Hkv][prefix_cap]
  *            (the quantize calls with B = 1); prefix_len >= 0
  *   k_*, v_* the sequences' own caches, seqlens_k int32 [B] their lengths, which may
