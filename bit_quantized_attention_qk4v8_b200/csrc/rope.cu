@@ -7,8 +7,8 @@
 // (4 * rotary bytes) is read once for up to 32 heads. Bound by the ALU, whose issue rate
 // it takes to 0.65 (the rotation's exact rounding, the two unpackings, the encoder): 4
 // x 8192 tokens of 32 heads 96 us, 0.57 of the copy peak; 2047 tokens of 64 heads, half of
-// the channels rotated, 18.5 us; 3 x 1601 tokens of 8 heads with three axes and the
-// Hadamard rotation 14 us; one token of 32 sequences and 32 heads 4 us.
+// the channels rotated, 19 us; 3 x 1601 tokens of 8 heads with three axes and the
+// Hadamard rotation 11.6 us; one token of 32 sequences and 32 heads 4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -364,11 +364,13 @@ inline RopeTiling rope_tiling(int B, int tokens, int H) {
     if (H < 3) t.hs_log2 = H - 1 < t.hs_log2 ? H - 1 : t.hs_log2;
     const int hs = 1 << t.hs_log2, ts = 4 >> t.hs_log2;
     t.token_groups = (tokens + ts - 1) / ts;
-    // Up to 8 steps over the heads an item, fewer while the items would not give
-    // every SM 32 warps.
+    // Up to 8 steps over the heads an item, fewer while the items would not give every SM
+    // 16 warps, two thirds of what it holds: with 32 asked for, an item's start (position, then
+    // cosines) is paid in two waves of short items (3 x 1601 tokens of 8 heads 13.8 us,
+    // here 11.6), with 8 too few warps hide each other's (13.6).
     int steps = 8;
     auto chunks = [&](int s) { return (H + s * hs - 1) / (s * hs); };
-    while (steps > 1 && static_cast<int64_t>(B) * t.token_groups * chunks(steps) < 148 * 32) steps >>= 1;
+    while (steps > 1 && static_cast<int64_t>(B) * t.token_groups * chunks(steps) < 148 * 16) steps >>= 1;
     t.heads = steps * hs;
     t.head_chunks = chunks(steps);
     return t;
