@@ -503,6 +503,11 @@ def attention_decode_bf16_paged(q: torch.Tensor, cache: PagedKV, max_seqlen: int
     return (out, lse) if return_lse else out
 
 
+def _empty(dtype, device, a, b, c, d):
+    """torch.empty of [a, b, c, d], as empty_strided (less host time)."""
+    return torch.empty_strided((a, b, c, d), (b * c * d, c * d, d, 1), dtype=dtype, device=device)
+
+
 def _check_dense(device, *tensors):
     for t in tensors:
         if t.device != device or not t.is_contiguous():
@@ -599,8 +604,7 @@ def quantize_qk_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tens
     rs = _rope_struct(rope, positions, B, T, dev)
     st = _int32_on(start, B, dev, "start")
     if out is None:
-        out = MXFP4(torch.empty((B, H, cap, 64), dtype=torch.uint8, device=dev),
-                    torch.empty((B, H, cap // 128, 512), dtype=torch.uint8, device=dev), B, H, cap, T)
+        out = MXFP4(_empty(torch.uint8, dev, B, H, cap, 64), _empty(torch.uint8, dev, B, H, cap // 128, 512), B, H, cap, T)
     with _on(dev):
         # (An empty x has a null pointer; no row of it is read.)
         check(lib().qk4v8_quantize_qk_rope(x.data_ptr() or out.codes.data_ptr(), B, T, H, D, x.stride(0), x.stride(1),
@@ -662,11 +666,11 @@ def _prefix_buffers(q: MXFP4, Hkv: int, prefix_len: int, max_seqlen: int, worksp
     dev = q.codes.device
     if workspace is None:
         need = decode_prefix_workspace_bytes(q.B, q.H, Hkv, q.length, prefix_len, max_seqlen)
-        workspace = torch.empty((max(16, need),), dtype=torch.uint8, device=dev)
+        workspace = torch.empty_strided((max(16, need),), (1,), dtype=torch.uint8, device=dev)
     else:
         _check_dense(dev, workspace)
     if out is None:
-        out = torch.empty((q.B, q.length, q.H, D), dtype=torch.bfloat16, device=dev)
+        out = _empty(torch.bfloat16, dev, q.B, q.length, q.H, D)
     elif out.dtype != torch.bfloat16 or out.device != dev or tuple(out.shape) != (q.B, q.length, q.H, D) or \
             not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor [B, nq, Hq, 128] on q's device")
