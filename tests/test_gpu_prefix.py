@@ -338,6 +338,36 @@ def test_serving_steps_of_all_of_it(Hq, Hkv, nq, hadamard):
         check(got, want)
 
 
+def test_pages_far_into_a_large_pool():
+    """Pages whose bytes lie past 2^32 of the pool: appended and attended to bit for bit as in a small pool."""
+    B, Hkv, Hq, nq, prefix, T = 3, 8, 16, 2, 200, 300
+    pages = (1 << 32) // (Hkv * 128 * 128) + 64          # 4.3 GB of V
+    if torch.cuda.mem_get_info()[0] < 9 << 30:
+        pytest.skip("needs 9 GB")
+    rng = np.random.default_rng(3)
+    mk = lambda *s: to_dev(f32_to_bf16(rng.standard_normal(s).astype(np.float32)))
+    pk, pv, k, v, q = mk(1, prefix, Hkv, 128), mk(1, prefix, Hkv, 128), mk(B, T, Hkv, 128), mk(B, T, Hkv, 128), mk(B, nq, Hq, 128)
+    rope = qk.Rope(torch.from_numpy(angles(prefix + T, 128)).cuda())
+    qp = qk.quantize_qk_rope(q, rope, start=torch.full((B,), prefix + T - nq, dtype=torch.int32, device="cuda"))
+    outs = []
+    for num in (16, pages):
+        perm = torch.arange(num - 1, num - 15, -1, dtype=torch.int32)
+        cache = qk.paged_kv(B, Hkv, num, perm[2:2 + 3 * B].reshape(B, 3))
+        head = qk.PagedKV(cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales,
+                          torch.zeros((1, Hkv, 32, 128), dtype=torch.bfloat16, device="cuda"), perm[None, :2].cuda(),
+                          torch.zeros(1, dtype=torch.int32, device="cuda"))
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        qk.kv_append_rope(head, pk, pv, rope, dev_status=status)
+        pos = torch.arange(prefix, prefix + T, dtype=torch.int32, device="cuda")[None].expand(B, T)
+        qk.kv_append_rope(cache, k, v, rope, positions=pos, dev_status=status)
+        outs.append(qk.attention_decode_prefix_paged(qp, cache, perm[:2].cuda(), prefix, max_seqlen=384, return_lse=True,
+                                                     dev_status=status))
+        assert int(status) == 0
+        if num == pages:
+            assert cache.v_codes.numel() > 1 << 32
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
 def dequantize_qk_maybe(bits, hadamard):
     """What the packed rows hold; rotated by the Hadamard matrix on both sides, Q K^T is what it is."""
     if not hadamard:
