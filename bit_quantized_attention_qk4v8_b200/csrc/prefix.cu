@@ -98,7 +98,7 @@ constexpr int kPxPvWarp = kPxFeedWarp + 3;
 constexpr int kPxExpandWarp = kPxSoftmaxWarps + 4;
 constexpr int kPxThreads = 32 * (kPxExpandWarp + 8);
 constexpr float kPxMove = 64.0f;            // m_O moves once a score passes it by 2^64
-constexpr float kPxMaxMove = 65536.0f;
+constexpr float kPxClear = 126.0f;          // a move by this much and more leaves nothing of O
 // The queries' scales are taken 2^-64 smaller (the softmax scale is 2^64 larger): so the scores that
 // a row gets from other sequences' keys, which share its tile, stay finite even where those hold what
 // the quantizer makes of an infinity or a NaN (6 * 2^126), and fma(s, scale, -inf) is -inf.
@@ -709,8 +709,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 if (i > 0) ok &= px_take(a_ref, seqno - 1, flag, m);
                 if (i == 0 || (hm > m && (m == -INFINITY || hm - m > kPxMove))) {
                     if (m > -INFINITY) {
-                        E = static_cast<int>(ceilf(fminf(hm - m, kPxMaxMove)));
-                        m += static_cast<float>(E);
+                        // By whole binades, which O can be scaled by; further than those reach, to the
+                        // score itself, and O is cleared: the move has no limit, so p stays below 2^64.
+                        const float up = hm - m;
+                        E = static_cast<int>(ceilf(fminf(up, kPxClear)));
+                        m = up < kPxClear ? m + static_cast<float>(E) : hm;
                     } else {
                         m = hm;
                     }

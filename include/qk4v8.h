@@ -504,6 +504,12 @@ QK4V8_API int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, 
  *            row with no key at all outputs 0 with lse = -inf. Sequences share tiles, not
  *            results: where one's own keys or values come from infinities or NaN, its
  *            rows are undefined and the others' are not touched.
+ *   range    scores (with softmax_scale, times log2 e) below 2^26 in magnitude, in any
+ *            order along the keys. Weights reach 2^64 above the first ones of a CTA's
+ *            run of keys before they are rescaled, so |v| summed over a row's keys has
+ *            to stay below 2^60. Query scales (of 32 channels) below 2^-63 count as
+ *            2^-63, which moves a score by less than 2^-16 while keys are below 2^40 in
+ *            magnitude and softmax_scale is the default.
  * Needs (Hq / Hkv) * nq <= 128. Two launches: the attention kernel over the prefix and
  * the own keys, and the merge of its partial results.
  *

@@ -138,6 +138,56 @@ def test_scores_that_pass_the_reference_by_far(order, prefix, lens):
     check(p.run(), p.reference())
 
 
+# Enough tiles that every CTA has a run of several: of a long prefix, and of the own keys of many sequences.
+RUNS = [(2, 8, 8, 1, 12000, [300, 0]), (24, 4, 4, 2, 128, [600 - 9 * i for i in range(24)])]
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("case", RUNS, ids=["prefix", "own"])
+@pytest.mark.parametrize("q_mult", [8.0, 30.0])
+def test_references_that_move_within_a_run_of_tiles(q_mult, case, paged):
+    """Every second tile's keys are small, and the others grow: a run's first maxima are passed by tens to hundreds of
+    binades again and again, by more and by less than O can be scaled by (2^-126)."""
+    p = Problem(*case, seed=40, paged=paged, q_mult=q_mult, k_mult=lambda j: np.where(j // 128 % 2 == 0, 1e-2, 0.2 + j / 4000))
+    check(p.run(), p.reference())
+
+
+def one_hot(p):
+    """Whether each row's softmax is one key's: the gap from its largest score to the next passes by 100 (e^-100 is lost in
+    any rounding here) what the two can be off by, 16 * 2^-24 of their terms' magnitudes each as in
+    ref_positions.attention_row. Also the least step up, in binades, from the keys of the even tiles to the odd ones'."""
+    q, none = dequantize_qk(p.q), np.zeros((p.Hkv, 0, 128))
+    pk = dequantize_qk(p.pk)[0][:, :p.prefix] if p.prefix else none
+    step = np.inf
+    for b, n in enumerate(p.lens):
+        own = dequantize_qk(p.k[b:b + 1, :n])[0] if n else none
+        odd = np.arange(p.prefix + n) // 128 % 2 == 1
+        for h in range(p.Hq):
+            kv = h // (p.Hq // p.Hkv)
+            for t in range(p.nq):
+                m = max(0, n - p.nq + t + 1)
+                k = np.concatenate((pk[kv], own[kv, :m]))
+                s = k @ q[b, h, t] / np.sqrt(128)
+                mag = (np.abs(k) @ np.abs(q[b, h, t])).max() / np.sqrt(128)
+                top = np.sort(s)[-2:]
+                if top[1] - top[0] < 100 + 2 * 16 * 2.0 ** -24 * mag:
+                    return False, 0.0
+                step = min(step, (top[1] - s[~odd[:len(s)]].max()) * np.log2(np.e))
+    return True, step
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("case", RUNS, ids=["prefix", "own"])
+def test_scores_that_jump_further_than_an_exponent_reaches(case, paged):
+    """Queries and keys of N(0, 1000^2), but the keys of every second tile a millionth as large: the largest scores pass a
+    run's first ones by a million binades. The softmax of such a row is one key's, so the output is that key's value,
+    rounded to bf16 once (the general bound, whose spread of values is 0 here)."""
+    p = Problem(*case, seed=41, paged=paged, q_mult=1000.0, k_mult=lambda j: np.where(j // 128 % 2 == 0, 1e-3, 1e3))
+    alone, step = one_hot(p)
+    assert alone and step > 3e5
+    check(p.run(), p.reference())
+
+
 @pytest.mark.parametrize("paged", [False, True])
 def test_nothing_behind_the_last_token_is_seen(paged):
     """NaN codes and NaN scales behind the lengths: not a bit of the result changes."""
