@@ -51,7 +51,7 @@
 //
 // Rows of several sequences share the tiles of own keys, so what one sequence's keys
 // and values hold must not reach the others' rows, which take them with weight 0: their scores
-// stay finite (kPxQShift), and V goes into bf16 without infinities and NaN. 5 us of the 283.
+// stay finite (kPxQShift), and their V goes into bf16 without infinities and NaN. 5 us of the 283.
 //
 // Warp roles (640 threads): warps 0..7 softmax and epilogue, 8 feeder (units, queries,
 // key tiles), 9 TMEM allocator and issuer of S, 10 issuer of D, 11 issuer of P V, 12..19 V
@@ -219,13 +219,16 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
     return d;
 }
 
-// Two values of V in bf16, infinities and NaN as the largest finite values: the rows of other
-// sequences take it with weight 0, and 0 times it has to be 0.
-__device__ __forceinline__ uint32_t px_v_bf16x2(float lo, float hi) {
+// Two values of V in bf16. Infinities become the largest finite values. So does a NaN of own keys
+// (kPxOwnLeast): the rows of other sequences take it with weight 0, and 0 times it has to be 0. A
+// NaN of the prefix, which every row averages, stays one (kPxPrefixLeast: the maximum with a NaN is
+// the other value).
+constexpr uint32_t kPxOwnLeast = 0xFF7FFF7Fu, kPxPrefixLeast = 0x7FFF7FFFu;
+__device__ __forceinline__ uint32_t px_v_bf16x2(float lo, float hi, uint32_t least) {
     uint32_t d;
     asm("{\n\t.reg .b32 t;\n\tcvt.rn.satfinite.bf16x2.f32 t, %1, %2;\n\tmax.bf16x2 %0, t, %3;\n\t}"
         : "=r"(d)
-        : "f"(hi), "f"(lo), "r"(0xFF7FFF7Fu));
+        : "f"(hi), "f"(lo), "r"(least));
     return d;
 }
 
@@ -1159,6 +1162,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     ok &= wait(full, f);
                     f ^= 1;
                 }
+                // (The entry is the tile's until the warps have read its D.)
+                const uint32_t least = tile_at(k >> 1)->rows >> 16 ? kPxOwnLeast : kPxPrefixLeast;
                 ok &= wait(S::kVEmpty + 8 * slot, ((k / kPxVSlots) & 1) ^ 1);
                 tc_fence_after();
                 __syncwarp();
@@ -1175,7 +1180,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     uint32_t w[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        w[e] = px_v_bf16x2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
+                        w[e] = px_v_bf16x2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]), least);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         sts128(row + (((4 * q + 2 * e0 + e) ^ (ch & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2],

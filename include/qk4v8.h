@@ -503,7 +503,8 @@ QK4V8_API int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, 
  *   out, lse, softmax_scale, dev_status and errors as for qk4v8_attention_decode. A
  *            row with no key at all outputs 0 with lse = -inf. Sequences share tiles, not
  *            results: where one's own keys or values come from infinities or NaN, its
- *            rows are undefined and the others' are not touched.
+ *            rows are undefined and the others' are not touched. A NaN among the prefix's
+ *            values is in every row's output, in its head and channel.
  *   range    scores (with softmax_scale, times log2 e) below 2^26 in magnitude, in any
  *            order along the keys. Weights reach 2^64 above the first ones of a CTA's
  *            run of keys before they are rescaled, so |v| summed over a row's keys has

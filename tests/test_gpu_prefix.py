@@ -243,6 +243,37 @@ def test_one_sequence_does_not_reach_another(where, bad):
     assert torch.equal(out[others], clean[0][others]) and torch.equal(lse[others], clean[1][others])
 
 
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_nan_in_the_prefix_reaches_every_row_that_averages_it(paged):
+    """Every row sees the prefix, so a NaN among its values is in every row's output, in its head and channel, and nowhere
+    else; as in the other decode calls."""
+    def problem(bad):
+        p = Problem(4, 8, 2, 2, 333, [5, 100, 0, 161], seed=12)
+        if bad:
+            p.pv[0, 70, 1, 9] = p.pv[0, 300, 0, 127] = 0x7FC0
+        q = Problem.__new__(Problem)
+        q.__dict__.update(p.__dict__)
+        q.pvp = qk.quantize_v(to_dev(p.pv), cap=p.pkp.cap, seqlens=torch.tensor([p.prefix]))
+        if paged:
+            pages = 3 + 4 * 2
+            q.paged, q.prefix_table = True, torch.tensor([7, 0, 9], dtype=torch.int32, device="cuda")
+            bt = torch.tensor([[1, 2], [3, 4], [5, 6], [8, 10]], dtype=torch.int32)
+            c = q.cache = qk.paged_kv(4, 2, pages, bt)
+            for at, kk, vv in ((q.prefix_table.long()[None], q.pkp, q.pvp), (bt.long().cuda(), q.kp, q.vp)):
+                for i in range(at.shape[1]):
+                    c.k_codes[at[:, i]] = kk.codes[:, :, i * 128:(i + 1) * 128]
+                    c.k_scales[at[:, i]] = kk.scales[:, :, i]
+                    c.v_codes[at[:, i]] = vv.codes[:, :, i]
+                    c.v_scales[at[:, i]] = vv.scales[:, :, i]
+            c.seqlens.copy_(q.sl)
+        return q
+    clean, (out, lse) = problem(False).run(), problem(True).run()
+    bad = torch.zeros(8, 128, dtype=torch.bool, device="cuda")
+    bad[4:, 9] = bad[:4, 127] = True
+    assert torch.isnan(out[:, :, bad]).all()
+    assert torch.equal(out[:, :, ~bad], clean[0][:, :, ~bad]) and torch.equal(lse, clean[1])
+
+
 def test_bounds_that_are_loose_or_cut():
     p = Problem(4, 8, 2, 1, 200, [5, 100, 0, 161], cap=1024)
     check(p.run(max_seqlen=1024), p.reference())
