@@ -259,6 +259,9 @@ struct KvAppendRopeArgs {
     int v_pages;  // pages that n tokens can touch
 };
 
+// A length that sequences can have; the others' are skipped and keep theirs.
+__device__ __forceinline__ bool append_length_ok(int L0, int max_pages) { return L0 >= 0 && L0 <= max_pages * 128; }
+
 // New tokens of sequence b: new_lens[b] (none: all n), held to 0..n.
 __device__ __forceinline__ int append_count(const KvAppendRopeArgs &a, int b) {
     if (!a.new_lens) return a.n;
@@ -300,7 +303,7 @@ __device__ __forceinline__ void append_k_rows(const KvAppendRopeArgs &a, uint32_
     int page = -1;
     // (L0 + t cannot pass 2^31 within the pages: L0 < max_pages * 128 < 2^31 - n.)
     if (mine) {
-        page = L0 <= a.max_pages * 128 ? page_of(a.block_table, a.max_pages, a.num_pages, b, L0 < 0 ? -1 : L0 + t) : -1;
+        page = append_length_ok(L0, a.max_pages) ? page_of(a.block_table, a.max_pages, a.num_pages, b, L0 + t) : -1;
         if (page < 0 && j == 0) flag_bad_page(a.status);
     }
     const bool live = page >= 0;
@@ -342,9 +345,10 @@ __device__ __forceinline__ void append_v_page(const KvAppendRopeArgs &a, int idx
     const int b = bh / a.H, h = bh - b * a.H;
     const int L0 = a.seqlens[b];
     const int m = append_count(a, b);
-    if (pg == 0 && h == 0 && threadIdx.x == 0 && a.seqlens_out) a.seqlens_out[b] = L0 + m;
+    const bool length_ok = append_length_ok(L0, a.max_pages);
+    if (pg == 0 && h == 0 && threadIdx.x == 0 && a.seqlens_out) a.seqlens_out[b] = length_ok ? L0 + m : L0;
     if (m == 0) return;
-    if (L0 < 0 || L0 > a.max_pages * 128) {
+    if (!length_ok) {
         if (threadIdx.x == 0) flag_bad_page(a.status);
         return;
     }
@@ -460,9 +464,9 @@ __global__ void __launch_bounds__(256, 3) kv_append_rope_kernel(const __grid_con
 }
 
 // seqlens[b] += new_lens[b] (held to 0..n) in place, after every reader of seqlens ran.
-__global__ void kv_advance_ragged_kernel(int32_t *seqlens, const int32_t *new_lens, int B, int n) {
+__global__ void kv_advance_ragged_kernel(int32_t *seqlens, const int32_t *new_lens, int B, int n, int max_pages) {
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
-    if (b < B) seqlens[b] += new_lens ? min(max(new_lens[b], 0), n) : n;
+    if (b < B && append_length_ok(seqlens[b], max_pages)) seqlens[b] += new_lens ? min(max(new_lens[b], 0), n) : n;
 }
 
 cudaError_t launch_kv_append_rope(const void *k, const void *v, int B, int n, int H, const int64_t (&ks)[3],
@@ -518,7 +522,7 @@ cudaError_t launch_kv_append_rope(const void *k, const void *v, int B, int n, in
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !in_place) return e;
-    kv_advance_ragged_kernel<<<(B + 255) / 256, 256, 0, stream>>>(seqlens_out, new_lens, B, n);
+    kv_advance_ragged_kernel<<<(B + 255) / 256, 256, 0, stream>>>(seqlens_out, new_lens, B, n, max_pages);
     return cudaGetLastError();
 }
 

@@ -151,6 +151,26 @@ def test_bad_pages_lengths_and_counts_are_reported_and_skipped():
     check(cache, turned, v, [T, 2, 4, 0, 1, T])
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_lengths_after_sequences_and_tokens_that_were_skipped(in_place):
+    """A sequence that is skipped (its length below 0 or past its pages) keeps its length; tokens without a page count, as
+    kv_append's do: the caller sees the status and has the numbers that it asked for."""
+    B, H, T = 6, 2, 50
+    k, v, table, axis, pos, rope, cache = make(B, H, T, 128, False, 1, False, 83, 2, 12)
+    cache.block_table[5, 0] = -1
+    lens = [0, -4, 2 * 128 + 1, 2 * 128, 230, 0]
+    cache.seqlens.copy_(torch.tensor(lens))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = cache.seqlens if in_place else torch.full((B,), -77, dtype=torch.int32, device="cuda")
+    new = torch.tensor([T, 7, 7, 3, T, 20], dtype=torch.int32, device="cuda")
+    rope = qk.Rope(torch.from_numpy(angles(300, 128)).cuda())
+    qk.kv_append_rope(cache, to_dev(k), to_dev(v), rope, new_lens=new, dev_status=status,
+                      seqlens_out=None if in_place else out)
+    assert int(status) == 1
+    assert out.cpu().tolist() == [T, -4, 2 * 128 + 1, 2 * 128 + 3, 230 + T, 20]
+    assert in_place or cache.seqlens.cpu().tolist() == lens
+
+
 def test_captured_appends():
     """A captured append, replayed for one token after the other on a stream of its own."""
     B, H, T = 4, 8, 70
