@@ -403,11 +403,11 @@ __device__ __forceinline__ void append_v_page(const KvAppendRopeArgs &a, int idx
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             w[i] = t32[(grp * 32 + i) * (kPitch / 2) + cp];
-            mx = __vmaxu2(mx, w[i] & 0x7FFF7FFFu);
+            mx = max_abs_number_bf16x2(w[i], mx);  // (a NaN does not set its group's scale)
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            X[q] = shared_exponent(q ? bf16_hi(mx) : bf16_lo(mx), 8);
+            X[q] = shared_exponent(fabsf(q ? bf16_hi(mx) : bf16_lo(mx)), 8);
             const float f = pow2_neg(X[q]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

@@ -138,6 +138,13 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// The same, but of a number and a NaN the number.
+__device__ __forceinline__ uint32_t max_abs_number_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Pairs 2i, 2i + 1 of the lane, from its two chunks' words: a, b the pairs' first and second values.
 template <bool kAdjacent>
 __device__ __forceinline__ void unpack_pairs(uint32_t u, uint32_t v, float2 &a, float2 &b) {

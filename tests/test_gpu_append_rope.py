@@ -151,6 +151,30 @@ def test_bad_pages_lengths_and_counts_are_reported_and_skipped():
     check(cache, turned, v, [T, 2, 4, 0, 1, T])
 
 
+def test_values_that_are_not_finite_are_packed_as_by_the_plain_append():
+    """A NaN or an infinity of a value leaves the rest of its group of 32 as kv_append and quantize_v pack it."""
+    B, H, T = 2, 3, 70
+    k, v, table, axis, pos, rope, cache = make(B, H, T, 128, False, 1, False, 84, 1, 2)
+    pos[:] = np.arange(T)
+    v[0, 5, 1, ::7] = 0x7FC0
+    v[0, 40, 2, 3:9] = 0xFFC1
+    v[1, 69, 0, ::2] = 0x7F80
+    v[1, 33] = 0xFF80
+    other = qk.paged_kv(B, H, 2, cache.block_table)
+    for a, b in zip((other.k_codes, other.k_scales, other.v_codes, other.v_scales), (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)):
+        a.copy_(b)
+    turned = to_dev(rotate(k, table, pos, axis))
+    kd, vd = to_dev(k), to_dev(v)
+    for a, b in ((0, 20), (20, 21), (21, 66), (66, T)):
+        qk.kv_append_rope(cache, kd[:, a:b], vd[:, a:b], rope)
+        qk.kv_append(other, turned[:, a:b], vd[:, a:b])
+    whole = qk.quantize_v(vd)
+    for b in range(B):
+        page = int(cache.block_table[b, 0])
+        assert torch.equal(other.v_codes[page, ..., :96], whole.codes[b, :, 0, :, :96])
+        assert torch.equal(cache.v_codes[page], other.v_codes[page]) and torch.equal(cache.v_scales[page], other.v_scales[page])
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_lengths_after_sequences_and_tokens_that_were_skipped(in_place):
     """A sequence that is skipped (its length below 0 or past its pages) keeps its length; tokens without a page count, as
