@@ -15,7 +15,12 @@
 // remainder e from a fused multiply-add, y = fma(x_a, c, -p) - e is within two
 // units in the last place of fp32, and rounds to the same bf16 value unless it
 // lies within 4 such units of a border between two (9 of 65536 values); those
-// pairs, and all of a lane with a result that is not finite, are done again in fp64.
+// pairs are done again in fp64. So are all of a lane with a result that is not finite, or
+// with a pair whose results are both below 2^-20: where both products are below 2^-101 the
+// remainders underflow, and a result that rounds to zero may come out with the wrong sign.
+// (With a result from 2^-20 up beside it, a cosine or sine would have to be below 2^-80 and
+// not 0, or 0 beside one below 2^-17: no rotation, whatever its scaling.) Rows of zeros take
+// that way as well: 137 us where others take 92.
 // The bf16 rounding itself is part of the operator: a model that rotates in
 // its bf16 activations and then quantizes gets the same bytes.
 #pragma once
@@ -145,6 +150,24 @@ __device__ __forceinline__ uint32_t max_abs_number_bf16x2(uint32_t a, uint32_t b
     return d;
 }
 
+// The least magnitude of two.
+__device__ __forceinline__ uint32_t min_abs_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Whether a magnitude of `low` is below 2^-20, or one of `big` an infinity or a NaN.
+__device__ __forceinline__ bool not_within_bf16x2(uint32_t low, uint32_t big) {
+    uint32_t d;
+    asm("{\n\t.reg .pred p, q, r, s;\n\t.reg .b32 l, b;\n\tabs.bf16x2 l, %1;\n\tabs.bf16x2 b, %2;\n\t"
+        "setp.lt.bf16x2 p|q, l, %3;\n\tsetp.geu.bf16x2 r|s, b, %4;\n\t"
+        "or.pred p, p, q;\n\tor.pred r, r, s;\n\tor.pred p, p, r;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(d)
+        : "r"(low), "r"(big), "r"(0x35803580u), "r"(0x7F807F80u));
+    return d != 0;
+}
+
 // Pairs 2i, 2i + 1 of the lane, from its two chunks' words: a, b the pairs' first and second values.
 template <bool kAdjacent>
 __device__ __forceinline__ void unpack_pairs(uint32_t u, uint32_t v, float2 &a, float2 &b) {
@@ -166,7 +189,7 @@ __device__ __forceinline__ void rotate_pairs(const RopeTrig &g, const uint32_t (
         return i < 2 ? w0[2 * i + second] : w1[2 * (i - 2) + second];
     };
     uint32_t near[4];  // least distance from a bf16 border, per half, offset to 0..8
-    uint32_t big = 0;  // largest magnitude
+    uint32_t big = 0, low = 0;  // largest magnitude; least of the pairs' larger ones
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 c = g.c[i], s = g.s[i], ns = make_float2(-s.x, -s.y);
@@ -182,10 +205,12 @@ __device__ __forceinline__ void rotate_pairs(const RopeTrig &g, const uint32_t (
         near[i] = __viaddmin_u16x2(__byte_perm(__float_as_uint(yb.x), __float_as_uint(yb.y), 0x5410), 0x80048004u, na);
         wa[i] = pack_bf16(ya.x, ya.y);
         wb[i] = pack_bf16(yb.x, yb.y);
-        big = i == 0 ? max_abs_bf16x2(wa[i], wb[i]) : max_abs_bf16x2(max_abs_bf16x2(wa[i], wb[i]), big);
+        const uint32_t top = max_abs_bf16x2(wa[i], wb[i]);
+        big = i == 0 ? top : max_abs_bf16x2(top, big);
+        low = i == 0 ? top : min_abs_bf16x2(top, low);
     }
     // (A result that is not finite in fp32 is not in bf16 either.)
-    const bool odd = (big & 0x7F80u) == 0x7F80u || (big & 0x7F800000u) == 0x7F800000u;
+    const bool odd = not_within_bf16x2(low, big);
     const uint32_t least = __vminu2(__vminu2(near[0], near[1]), __vminu2(near[2], near[3]));
     if (odd || (least & 0xFFFFu) <= 8u || (least >> 16) <= 8u) {
 #pragma unroll

@@ -99,6 +99,26 @@ def test_special_values(case):
         check(got, expected(bits, table, pos, None, False, hadamard), T)
 
 
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("others", [0x0000, 0x3F80])
+def test_results_that_underflow_keep_their_sign(adjacent, others):
+    """x_a c - x_b s = -2^-152 and its like: below what fp32 holds, so the code is a zero, whose sign is the exact value's."""
+    rng = np.random.default_rng(17)
+    B, T, H = 2, 16, 5
+    bits = np.full((B, T, H, 128), others, np.uint16)
+    at = np.arange(0, 64, 3)
+    table = np.zeros((T, 64, 2), np.float32)
+    table[..., 0], table[..., 1] = 1.0, 0.0
+    # Subnormal values of up to two bits with cosines and sines of 2^-14 .. 2^-22: results of 2^-155 .. 2^-144, both signs.
+    small = lambda: (rng.integers(1, 4, (B, T, H, len(at))) | (rng.integers(0, 2, (B, T, H, len(at))) << 15)).astype(np.uint16)
+    a, b = (2 * at, 2 * at + 1) if adjacent else (at, at + 64)
+    bits[..., a], bits[..., b] = small(), small()
+    table[:, at] = np.ldexp(rng.choice([-1.0, 1.0], (T, len(at), 2)), -rng.integers(14, 23, (T, len(at), 2))).astype(np.float32)
+    pos = np.arange(T, dtype=np.int32)[None, None].repeat(B, 1)
+    got = qk.quantize_qk_rope(to_dev(bits), qk.Rope(torch.from_numpy(table).cuda(), adjacent=adjacent))
+    check(got, oracle.quantize_qk(rotate(bits, table, pos, None, adjacent)), T)
+
+
 def test_strides_positions_and_starts():
     """Heads of a fused projection, positions of every shape, starts: the same rows."""
     rng = np.random.default_rng(11)
