@@ -1120,6 +1120,11 @@ int qk4v8_kv_append_rope(const void *k_new, const void *v_new, int B, int n_new,
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
         !aligned16(v_scales) || !aligned16(v_tail))
         return set_error(QK4V8_ERR_INVALID_ARG, "K/V inputs, pools and v_tail must be 16-byte aligned");
+    // Lengths are written while other blocks read theirs (in place, after all of them have).
+    auto overlap = [&](const int32_t *a, const int32_t *b) { return a && b && a < b + B && b < a + B; };
+    if ((seqlens_out != seqlens && (overlap(seqlens_out, seqlens) || overlap(seqlens_out, new_lens))) ||
+        (seqlens_out == seqlens && new_lens != seqlens && overlap(seqlens, new_lens)))
+        return set_error(QK4V8_ERR_INVALID_ARG, "seqlens_out must be seqlens itself or an array beside seqlens and new_lens");
     int64_t ks[3], vs[3];
     for (int i = 0; i < 3; ++i) {
         ks[i] = k_strides[i];

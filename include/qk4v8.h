@@ -471,8 +471,9 @@ QK4V8_API int qk4v8_quantize_qk_rope(const void *x, int B, int S, int H, int d, 
  *   new_lens  int32 [B] (device, nullable: n_new for all): the sequence's first
  *             new_lens[b] tokens are appended, 0 touches nothing of it. A count
  *             outside 0..n_new is held to that range and reported in *dev_status.
- *   seqlens_out  (device, nullable, may be seqlens) receives seqlens[b] + new_lens[b];
- *             tokens that are skipped for want of a page count, as qk4v8_kv_append's do
+ *   seqlens_out  (device, nullable, may be seqlens, else overlaps neither it nor
+ *             new_lens) receives seqlens[b] + new_lens[b]; tokens that are skipped for
+ *             want of a page count, as qk4v8_kv_append's do
  *   pages, v_tail, hadamard_k, dev_status and errors as for qk4v8_kv_append: the pages
  *   hold what qk4v8_quantize_qk_rope and qk4v8_quantize_v of the whole sequence give,
  *   after any run of appends by either call. A token without a valid page is skipped

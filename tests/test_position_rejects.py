@@ -128,3 +128,12 @@ def test_workspace_size(lib):
     for bad in ((0, 8, 2, 1, 1, 1), (1, 7, 2, 1, 1, 1), (1, 8, 2, 9, 1, 1), (1, 8, 2, 1, -1, 1), (1, 256, 1, 1, 1, 1),
                 (1 << 20, 8, 8, 1, 2**31 - 1, 0)):
         assert size(*bad) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=FAKE + 4, lens=FAKE, B=2), dict(out=FAKE, lens=FAKE + 4, B=2), dict(out=FAKE + 64, new=FAKE + 64),
+    dict(out=FAKE + 64, new=FAKE + 68, B=2), dict(out=FAKE, lens=FAKE, new=FAKE + 4, B=2)])
+def test_lengths_that_would_be_read_and_written_at_once(lib, kw):
+    """seqlens_out over a part of seqlens, or over new_lens: other blocks still read those while they are written."""
+    assert append(lib, **kw) == INVALID
+    assert b"seqlens_out" in lib.qk4v8_last_error()
