@@ -93,7 +93,7 @@ _HERE = contextlib.nullcontext()
 
 def _on(device):
     """The device as the current one; no switch (1.5 us of host time) when it is that already."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _check_bf16(x: torch.Tensor, name: str):
@@ -104,6 +104,9 @@ def _check_bf16(x: torch.Tensor, name: str):
 def _seqlens(seqlens, B, device):
     if seqlens is None:
         return None
+    if torch.is_tensor(seqlens) and seqlens.dtype is torch.int32 and seqlens.device == device and seqlens.numel() == B and \
+            seqlens.is_contiguous():
+        return seqlens
     if not torch.is_tensor(seqlens):
         seqlens = torch.tensor(seqlens, dtype=torch.int32)
     seqlens = seqlens.to(device=device, dtype=torch.int32).contiguous()
@@ -508,10 +511,58 @@ def _empty(dtype, device, a, b, c, d):
     return torch.empty_strided((a, b, c, d), (b * c * d, c * d, d, 1), dtype=dtype, device=device)
 
 
-def _check_dense(device, *tensors):
-    for t in tensors:
-        if t.device != device or not t.is_contiguous():
-            raise ValueError("packed buffers must be contiguous and on one device")
+_I32, _BF16 = torch.int32, torch.bfloat16
+
+
+def _misfit(device, name, t, what, nbytes):
+    got = "none" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}"
+    return ValueError(f"{name} must be a contiguous {what} tensor of {nbytes} bytes on {device}, got {got}")
+
+
+def _check_packed(device, name, x, row):
+    """codes (row bytes a token) and scales of a packed tensor: that what the call reads or writes is there. (By their
+    bytes, in one expression: half of a short call's host time went to comparing types and shapes one by one.)"""
+    c, s, i = x.codes, x.scales, device.index
+    n = x.B * x.H * x.cap
+    if c.nbytes == n * row and s.nbytes == n * 4 and c.get_device() == i and s.get_device() == i and \
+            c.is_contiguous() and s.is_contiguous():
+        return
+    for part, t, need in ((name + ".codes", c, n * row), (name + ".scales", s, n * 4)):
+        if t.nbytes != need or t.device != device or not t.is_contiguous():
+            raise _misfit(device, part, t, "uint8", need)
+
+
+def _check_cache(device, cache, tail):
+    """A paged cache's buffers (the staged rows if `tail`), as _check_packed; its pages, heads, sequences and pages of a
+    sequence."""
+    kc, ks, vc, vs, bt, sl = cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, cache.block_table, cache.seqlens
+    if kc.dim() != 4 or bt.dim() != 2:
+        raise ValueError("the cache must have k_codes [pages, Hkv, 128, 64] and block_table [B, max_pages]")
+    P, H, _, _ = kc.shape
+    B, most = bt.shape
+    i, n, t = device.index, P * H, cache.v_tail if tail else None
+    if bt.dtype is _I32 and sl.dtype is _I32 and kc.nbytes == n * 8192 and ks.nbytes == n * 512 and \
+            vc.nbytes == n * 16384 and vs.nbytes == n * 512 and sl.nbytes == B * 4 and kc.get_device() == i and \
+            ks.get_device() == i and vc.get_device() == i and vs.get_device() == i and bt.get_device() == i and \
+            sl.get_device() == i and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and \
+            vs.is_contiguous() and bt.is_contiguous() and sl.is_contiguous() and (
+                not tail or (t is not None and t.dtype is _BF16 and t.nbytes == B * H * 8192 and t.get_device() == i and
+                             t.is_contiguous())):
+        return P, H, B, most
+    for name, x, dtype, need in (("k_codes", kc, kc.dtype, n * 8192), ("k_scales", ks, ks.dtype, n * 512),
+                                 ("v_codes", vc, vc.dtype, n * 16384), ("v_scales", vs, vs.dtype, n * 512),
+                                 ("block_table", bt, _I32, B * most * 4), ("seqlens", sl, _I32, B * 4)):
+        if x.dtype is not dtype or x.nbytes != need or x.device != device or not x.is_contiguous():
+            raise _misfit(device, "the cache's " + name, x, "int32" if dtype is _I32 else "uint8", need)
+    raise _misfit(device, "the cache's v_tail", t, "bfloat16", B * H * 8192)
+
+
+def _status(t: Optional[torch.Tensor], device):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.device != device or t.numel() < 1:
+        raise ValueError("dev_status must be an int32 tensor on the inputs' device")
+    return t.data_ptr()
 
 
 # ----------------------------------------------------------------------------------------------------------
@@ -596,7 +647,7 @@ def quantize_qk_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tens
     if out is not None:
         if out.B != B or out.H != H or (cap is not None and cap != out.cap):
             raise ValueError("out must be a packed tensor of the same B, H and capacity")
-        _check_dense(dev, out.codes, out.scales)
+        _check_packed(dev, "out", out, 64)
         cap = out.cap
     elif cap is None:
         cap = round_cap(T)
@@ -610,7 +661,7 @@ def quantize_qk_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tens
         check(lib().qk4v8_quantize_qk_rope(x.data_ptr() or out.codes.data_ptr(), B, T, H, D, x.stride(0), x.stride(1),
                                            x.stride(2), _ptr(sl), st, ctypes.addressof(rs), int(bool(hadamard)), cap,
                                            int(bool(pad)), out.codes.data_ptr(), out.scales.data_ptr(),
-                                           _ptr(dev_status), _stream(dev)), "qk4v8_quantize_qk_rope")
+                                           _status(dev_status, dev), _stream(dev)), "qk4v8_quantize_qk_rope")
     out.length = T
     return out
 
@@ -628,17 +679,13 @@ def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rop
     positions as for quantize_qk_rope; without them a token is at its place in the sequence.
     cache.seqlens advances on the device, unless seqlens_out (int32 [B]) receives the new lengths."""
     _check_bf16(k_new, "k_new")
-    _check_bf16(v_new, "v_new")
     shape, dev = k_new.shape, k_new.device
     B, n_new, Hkv, _ = shape
-    if v_new.shape != shape or v_new.device != dev:
-        raise ValueError("k_new and v_new must have the same shape and device")
-    num_pages, heads = cache.k_codes.shape[:2]
-    rows, max_pages = cache.block_table.shape
+    if v_new.dtype is not _BF16 or v_new.shape != shape or v_new.device != dev or v_new.stride(3) != 1:
+        raise ValueError("v_new must be a bf16 tensor with k_new's shape and device and unit channel stride")
+    num_pages, heads, rows, max_pages = _check_cache(dev, cache, True)
     if B != rows or Hkv != heads:
         raise ValueError("k_new must be [cache.B, n_new, cache.Hkv, 128]")
-    _check_dense(dev, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, cache.v_tail, cache.block_table,
-                 cache.seqlens)
     rs = _rope_struct(rope, positions, B, n_new, dev)
     nl = _int32_on(new_lens, B, dev, "new_lens")
     lens = cache.seqlens.data_ptr()
@@ -650,7 +697,7 @@ def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rop
                                          cache.block_table.data_ptr(), max_pages, num_pages,
                                          cache.k_codes.data_ptr(), cache.k_scales.data_ptr(),
                                          cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), cache.v_tail.data_ptr(),
-                                         int(cache.hadamard_k), _ptr(dev_status), _stream(dev)),
+                                         int(cache.hadamard_k), _status(dev_status, dev), _stream(dev)),
               "qk4v8_kv_append_rope")
     return cache
 
@@ -667,8 +714,8 @@ def _prefix_buffers(q: MXFP4, Hkv: int, prefix_len: int, max_seqlen: int, worksp
     if workspace is None:
         need = decode_prefix_workspace_bytes(q.B, q.H, Hkv, q.length, prefix_len, max_seqlen)
         workspace = torch.empty_strided((max(16, need),), (1,), dtype=torch.uint8, device=dev)
-    else:
-        _check_dense(dev, workspace)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on q's device")
     if out is None:
         out = _empty(torch.bfloat16, dev, q.B, q.length, q.H, D)
     elif out.dtype != torch.bfloat16 or out.device != dev or tuple(out.shape) != (q.B, q.length, q.H, D) or \
@@ -700,8 +747,11 @@ def attention_decode_prefix(q: MXFP4, k_prefix: MXFP4, v_prefix: MXFP8V, k: MXFP
         raise ValueError("k and v must be packed tensors of q's batch with the same heads and capacity")
     if not isinstance(v, MXFP8V) or not isinstance(v_prefix, MXFP8V):
         raise ValueError("v and v_prefix must be MXFP8 (MXFP8V)")
-    _check_dense(dev, q.codes, q.scales, k_prefix.codes, k_prefix.scales, v_prefix.codes, v_prefix.scales, k.codes,
-                 k.scales, v.codes, v.scales)
+    _check_packed(dev, "q", q, 64)
+    _check_packed(dev, "k_prefix", k_prefix, 64)
+    _check_packed(dev, "v_prefix", v_prefix, D)
+    _check_packed(dev, "k", k, 64)
+    _check_packed(dev, "v", v, D)
     prefix_len = k_prefix.length if prefix_len is None else int(prefix_len)
     max_seqlen = k.cap if max_seqlen is None else int(max_seqlen)
     sl = _seqlens(seqlens_k, B, dev)
@@ -712,7 +762,7 @@ def attention_decode_prefix(q: MXFP4, k_prefix: MXFP4, v_prefix: MXFP8V, k: MXFP
             k_prefix.scales.data_ptr(), v_prefix.codes.data_ptr(), v_prefix.scales.data_ptr(), prefix_len, k_prefix.cap,
             k.codes.data_ptr(), k.scales.data_ptr(), v.codes.data_ptr(), v.scales.data_ptr(), k.H, k.cap, _ptr(sl),
             max_seqlen, int(bool(causal_in_block)), float(softmax_scale or 0.0), ws.data_ptr(), ws_bytes, out.data_ptr(),
-            _ptr(lse), _ptr(dev_status), _stream(dev)), "qk4v8_attention_decode_prefix")
+            _ptr(lse), _status(dev_status, dev), _stream(dev)), "qk4v8_attention_decode_prefix")
     return (out, lse) if return_lse else out
 
 
@@ -727,20 +777,20 @@ def attention_decode_prefix_paged(q: MXFP4, cache: PagedKV, prefix_table: torch.
     dev = q.codes.device
     B, Hq, nq = q.B, q.H, q.length
     prefix_len, max_seqlen = int(prefix_len), int(max_seqlen)
-    if cache.B != B:
+    num_pages, Hkv, rows, max_pages = _check_cache(dev, cache, False)
+    if rows != B:
         raise ValueError("the cache must hold q's batch")
-    _check_dense(dev, q.codes, q.scales, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales,
-                 cache.block_table, cache.seqlens)
+    _check_packed(dev, "q", q, 64)
     if prefix_table.dtype != torch.int32 or prefix_table.device != dev or prefix_table.dim() != 1 or \
             not prefix_table.is_contiguous() or prefix_table.shape[0] * 128 < prefix_len:
         raise ValueError("prefix_table must be a contiguous int32 tensor of the prefix's pages on q's device")
-    ws, ws_bytes, out, lse = _prefix_buffers(q, cache.Hkv, prefix_len, max_seqlen, workspace, out, lse, return_lse)
+    ws, ws_bytes, out, lse = _prefix_buffers(q, Hkv, prefix_len, max_seqlen, workspace, out, lse, return_lse)
     with _on(dev):
         check(lib().qk4v8_attention_decode_prefix_paged(
             q.codes.data_ptr(), q.scales.data_ptr(), B, Hq, nq, q.cap, cache.k_codes.data_ptr(),
-            cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), cache.Hkv, cache.num_pages,
-            prefix_table.data_ptr(), prefix_len, cache.block_table.data_ptr(), cache.max_pages,
+            cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), Hkv, num_pages,
+            prefix_table.data_ptr(), prefix_len, cache.block_table.data_ptr(), max_pages,
             cache.seqlens.data_ptr(), max_seqlen, int(bool(causal_in_block)), float(softmax_scale or 0.0),
-            ws.data_ptr(), ws_bytes, out.data_ptr(), _ptr(lse), _ptr(dev_status), _stream(dev)),
+            ws.data_ptr(), ws_bytes, out.data_ptr(), _ptr(lse), _status(dev_status, dev), _stream(dev)),
             "qk4v8_attention_decode_prefix_paged")
     return (out, lse) if return_lse else out
