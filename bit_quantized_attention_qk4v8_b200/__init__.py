@@ -593,6 +593,18 @@ class Rope:
                 raise ValueError("pair_axis must have rotary_dim / 2 entries of 0..3")
             self._axes, self.n_axes = (ctypes.c_uint8 * len(axes))(*axes), max(axes) + 1
 
+    def __setattr__(self, name, value):
+        """A table or axes set later are checked as the first ones (the library reads an axis for each pair of the table)."""
+        later = name in ("table", "pair_axis") and "_axes" in self.__dict__
+        before = self.__dict__.copy()
+        self.__dict__[name] = value
+        if later:
+            try:
+                self.__post_init__()
+            except Exception:
+                self.__dict__.update(before)
+                raise
+
     @property
     def rotary_dim(self) -> int:
         return 2 * self.table.shape[1]

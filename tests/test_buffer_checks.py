@@ -155,3 +155,25 @@ def test_status(calls, status):
     refused(calls, attend_paged, cache(), dev_status=s)
     refused(calls, attend, dev_status=s)
     refused(calls, rotate, dev_status=s)
+
+
+def test_a_rope_that_is_changed_later(calls):
+    """The table and the pairs' axes are checked against each other whenever one is set, as at first: the library reads an
+    axis for each pair of the table."""
+    f32 = lambda *s: torch.empty(s, dtype=torch.float32, device="cuda:0")
+    r = qk.Rope(f32(300, 32, 2), pair_axis=[0] * 16 + [1] * 16)
+    for name, value in (("table", f32(300, 64, 2)), ("table", f32(300, 32, 2).double()), ("table", torch.empty(300, 32, 2)),
+                        ("table", f32(32, 300, 2).transpose(0, 1)), ("pair_axis", [0] * 31), ("pair_axis", [4] * 32)):
+        old = getattr(r, name)
+        with pytest.raises(ValueError):
+            setattr(r, name, value)
+        assert getattr(r, name) is old and r.n_axes == 2 and r.rotary_dim == 64
+    r.pair_axis = None
+    assert r.n_axes == 1
+    r.table = f32(500, 64, 2)
+    r.pair_axis = [2] * 64
+    assert r.n_axes == 3 and r.rotary_dim == 128
+    rotate_by = lambda: qk.quantize_qk_rope(bf16(B, N, H, 128), r, positions=i32(3, B, N))
+    rotate_by()
+    r.pair_axis = [3] * 64
+    refused(calls, rotate_by)      # positions on three axes
