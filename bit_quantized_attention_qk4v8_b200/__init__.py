@@ -688,7 +688,8 @@ def kv_append_rope(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor, rop
     sequences (qk4v8_kv_append_rope).
 
     new_lens: int32 [B], the sequence's first new_lens[b] tokens are appended (None: all n_new).
-    positions as for quantize_qk_rope; without them a token is at its place in the sequence.
+    positions as for quantize_qk_rope; without them a token is at its place in the sequence, which is its position unless
+    the sequence goes on behind a prefix held elsewhere (attention_decode_prefix_paged): then give prefix_len + place.
     cache.seqlens advances on the device, unless seqlens_out (int32 [B]) receives the new lengths."""
     _check_bf16(k_new, "k_new")
     shape, dev = k_new.shape, k_new.device
@@ -785,7 +786,8 @@ def attention_decode_prefix_paged(q: MXFP4, cache: PagedKV, prefix_table: torch.
                                   lse: Optional[torch.Tensor] = None, return_lse: bool = False,
                                   dev_status: Optional[torch.Tensor] = None):
     """attention_decode_prefix over a page pool: prefix_table int32 [pages] lists the prefix's pages, the cache's
-    block_table and seqlens hold the sequences' own tokens (qk4v8_attention_decode_prefix_paged)."""
+    block_table and seqlens hold the sequences' own tokens (qk4v8_attention_decode_prefix_paged), whose keys stand at
+    positions from prefix_len on: kv_append_rope into such a cache needs its `positions`."""
     dev = q.codes.device
     B, Hq, nq = q.B, q.H, q.length
     prefix_len, max_seqlen = int(prefix_len), int(max_seqlen)

@@ -467,7 +467,8 @@ QK4V8_API int qk4v8_quantize_qk_rope(const void *x, int B, int S, int H, int d, 
  * tokens per sequence.
  *   k_new, v_new  bf16 [B][n_new][Hkv][128], strides {batch, token, head} each
  *   rope      as above; without positions, a token is at its place in the sequence,
- *             seqlens[b] + t
+ *             seqlens[b] + t (behind a shared prefix, see below, give positions of
+ *             prefix_len + seqlens[b] + t)
  *   new_lens  int32 [B] (device, nullable: n_new for all): the sequence's first
  *             new_lens[b] tokens are appended, 0 touches nothing of it. A count
  *             outside 0..n_new is held to that range and reported in *dev_status.

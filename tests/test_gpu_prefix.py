@@ -419,6 +419,44 @@ def test_serving_steps_of_all_of_it(Hq, Hkv, nq, hadamard):
         check(got, want)
 
 
+def test_the_documented_loop_over_a_shared_prefix():
+    """The user guide's lines, from the rotary positions to the attention, run as they stand for three steps of a batch:
+    against 64 bits with each token at its place behind the prefix."""
+    import re
+    from pathlib import Path
+    text = (Path(qk.__file__).resolve().parents[1] / "README.md").read_text()
+    lines = re.search(r"^rope = qk\.Rope\(.*?^out = qk\.attention_decode_prefix_paged\([^\n]*$", text, re.S | re.M).group(0)
+    B, Hq, Hkv, nq, prefix, steps, max_pos = 4, 8, 2, 2, 300, 3, 512
+    rng = np.random.default_rng(23)
+    mk = lambda *s: f32_to_bf16(rng.standard_normal(s).astype(np.float32))
+    pk, pv, k, v, q = mk(1, prefix, Hkv, 128), mk(1, prefix, Hkv, 128), mk(B, nq * steps, Hkv, 128), mk(
+        B, nq * steps, Hkv, 128), mk(B, nq * steps, Hq, 128)
+    pages = torch.tensor([5, 0, 2], dtype=torch.int32, device="cuda")
+    cache = qk.paged_kv(B, Hkv, 8, torch.tensor([[1], [3], [4], [6]], dtype=torch.int32))
+    head = qk.PagedKV(cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales,
+                      torch.zeros((1, Hkv, 32, 128), dtype=torch.bfloat16, device="cuda"), pages[None],
+                      torch.zeros(1, dtype=torch.int32, device="cuda"))
+    qk.kv_append_rope(head, to_dev(pk), to_dev(pv), qk.Rope(qk.rope_table(max_pos)))
+    table = qk.rope_table(max_pos).cpu().numpy()
+    n = torch.full((B,), nq, dtype=torch.int32, device="cuda")
+    turned = rotate(k, table, (prefix + np.arange(nq * steps))[None, None].repeat(B, 1))
+    for s in range(steps):
+        at = slice(s * nq, (s + 1) * nq)
+        env = dict(qk=qk, torch=torch, cache=cache, max_pos=max_pos, q_step=to_dev(q[:, at]), k_step=to_dev(k[:, at]),
+                   v_step=to_dev(v[:, at]), n=n, prefix_pages=pages, prefix_len=prefix, max_seqlen=128, B=B, Hq=Hq, Hkv=Hkv,
+                   nq=nq)
+        exec(lines, env)
+        seen = (s + 1) * nq
+        assert cache.seqlens.cpu().tolist() == [seen] * B
+        pos = (prefix + np.arange(s * nq, seen))[None, None].repeat(B, 1)
+        want = prefix_attention(dequantize_qk(rotate(q[:, at], table, pos)),
+                                dequantize_qk(rotate(pk, table, np.arange(prefix)[None, None]))[0], dequantize_v(pv)[0],
+                                [dequantize_qk(turned[b:b + 1, :seen])[0] for b in range(B)],
+                                [dequantize_v(v[b:b + 1, :seen])[0] for b in range(B)])
+        d = np.abs(env["out"].float().cpu().numpy().astype(np.float64) - want[0])
+        assert (d <= want[2]).all(), f"step {s}: worst {np.max(d / want[2]):.3g} of its bound"
+
+
 def test_pages_far_into_a_large_pool():
     """Pages whose bytes lie past 2^32 of the pool: appended and attended to bit for bit as in a small pool."""
     B, Hkv, Hq, nq, prefix, T = 3, 8, 16, 2, 200, 300
