@@ -1256,7 +1256,7 @@ int decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq
             return st;
         p.own = 1;
         // Lengths past max_seqlen are cut to it: no read behind the cache or its block table.
-        p.own_cap = max_seqlen;
+        p.own_most = max_seqlen;
         p.own_blocks = map_cap / 128;
         p.k_scales = k_scales;
         p.v_scales = v_scales;
@@ -1269,7 +1269,6 @@ int decode_prefix(const uint8_t *q_codes, const uint8_t *q_scales, int B, int Hq
     p.num_pages = pages.num_pages;
     p.q_codes = q_codes;
     p.q_scales = q_scales;
-    p.B = B;
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.G = Hq / Hkv;

@@ -58,11 +58,12 @@
 // expansion. The softmax warps hold 128 scores and get 168 registers, the others 48
 // (256 * 168 + 384 * 48 = the 640 * 96 of the launch).
 //
-// Measured (kernel, cold L2; the merge in brackets): 64 sequences of 64 query heads over 8 KV
-// heads with 8 query tokens, 16384 shared and up to 512 own keys: 283 us (12), 0.99 PFLOP/s;
-// 32 sequences of 32 heads, 8192 shared and up to 1024 own keys in pages: 30 us (4); 13 of
-// 20 heads with 3 tokens, 5003 and up to 777: 17 us (4); 4 of 32 heads, 1000 and up to 100:
-// 11 us (3.5). A tile takes 1.2 us in the long run, twice its exponentials. No one part is
+// Measured, both launches (with a cold L2 and the events' own 5 us): 64 sequences of 64 query heads
+// over 8 KV heads with 8 query tokens, 16384 shared and up to 512 own keys: 309 us, and 296 a
+// call in a row of calls, 0.94 PFLOP/s; 32 sequences of 32 heads, 8192 shared and up to 1024
+// own keys in pages: 42 us; 13 of 20 heads with 3 tokens, 5003 and up to 777: 29 us; 4 of 32
+// heads, 1000 and up to 100: 21.5 us. In a profiler's trace, as the comparisons here and below,
+// this kernel and the merge take 283 + 12, 30 + 4, 17 + 4 and 11 + 3.5 us. A tile takes 1.2 us in the long run, twice its exponentials. No one part is
 // the rest: of 278 us (before V's and the scores' guards), 264 are left without the exponentials,
 // 273 without the expansion, 271 with a quarter of P V, 239 without any softmax work; the roles' loops are chains of dependent
 // instructions, each close to the tile's time. In the short cases 6 to 8 us are the start
@@ -355,7 +356,7 @@ constexpr int kPxUnitCost = 1;  // a unit's start and end, in tiles
 
 // Sequence b's own keys.
 __device__ __forceinline__ int px_own_len(const PrefixParams &p, int b) {
-    return p.own ? imax(0, imin(p.seqlens[b], p.own_cap)) : 0;
+    return p.own ? imax(0, imin(p.seqlens[b], p.own_most)) : 0;
 }
 
 // n / d for 0 <= n < 2^30, 1 <= d <= 128, with m = ceil(2^32 / d): the product's high word is the

@@ -107,7 +107,7 @@ cudaError_t launch_kv_append(const void *k, const void *v, int B, int n_new, int
 // Shared-prefix decode (prefix.cu).
 struct PrefixParams {
     const uint8_t *q_codes, *q_scales;            // [B][Hq][q_cap]
-    int B, Hq, Hkv, G, nq, q_cap;
+    int Hq, Hkv, G, nq, q_cap;
     int gq;                                       // G * nq
     uint32_t m_gq, m_nq;                          // ceil(2^32 / gq), ceil(2^32 / nq), for px_div
     int rows, row_tiles;                          // query rows of a KV head (B * G * nq), and 128-row tiles
@@ -118,8 +118,9 @@ struct PrefixParams {
     int len, tiles, prefix_blocks;
     const uint8_t *p_k_scales, *p_v_scales;
     const int32_t *prefix_table;
-    // The sequences' own keys (own = 0: none), contiguous [B][Hkv][own_cap] or paged.
-    int own, own_cap, own_blocks;
+    // The sequences' own keys (own = 0: none), contiguous [B][Hkv][own_blocks * 128] or paged;
+    // lengths past own_most are cut to it.
+    int own, own_most, own_blocks;
     const uint8_t *k_scales, *v_scales;
     const int32_t *block_table, *seqlens;
     int max_pages, num_pages;
