@@ -239,9 +239,10 @@ cudaError_t launch_kv_append(const void *k, const void *v, int B, int n_new, int
 // 512 bytes read and 200 written per new token and head; a single token of a sequence
 // rewrites its open group, 4 KB per head. A long append is bound by the K rows'
 // instructions and the V pages' trips to memory, which is why the two kinds of CTA lie
-// evenly among each other: 8192 tokens of 8 heads and 4 sequences take 53.6 us (0.58 of
-// the copy peak; 66.5 with the V pages last and one token by four heads a K step). One
-// token of 64 sequences and 8 heads: 7.4 us, a chain of length, page and row.
+// evenly among each other: 8192 tokens of 8 heads and 4 sequences take 52 us a call in a row of
+// calls (0.60 of the copy peak), 58 with a cold L2. (In a profiler's trace 53.6, and 66.5 with
+// the V pages last and one token by four heads a K step.) One token of 64 sequences and 8
+// heads: 11 us with a cold L2, 5 of them the events' own, a chain of length, page and row.
 struct KvAppendRopeArgs {
     const __nv_bfloat16 *k, *v;
     int B, n, H;

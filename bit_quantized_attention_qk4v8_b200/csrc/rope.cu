@@ -4,11 +4,12 @@
 // rotated tensor is written and read once more (512 of 836 bytes a row).
 //
 // A row of 128 channels is 256 bytes in and 68 out; the table row of a token
-// (4 * rotary bytes) is read once for up to 32 heads. Bound by the ALU, whose issue rate
-// it takes to 0.65 (the rotation's exact rounding, the two unpackings, the encoder): 4
-// x 8192 tokens of 32 heads 96 us, 0.57 of the copy peak; 2047 tokens of 64 heads, half of
-// the channels rotated, 19 us; 3 x 1601 tokens of 8 heads with three axes and the
-// Hadamard rotation 11.6 us; one token of 32 sequences and 32 heads 4 us.
+// (4 * rotary bytes) is read once for up to 32 heads. Bound by its instructions (the rotation's
+// exact rounding, the two unpackings, the encoder: 250 a step of four rows, ALU pipe 0.66
+// and issue 0.72 busy at 24 warps an SM): 4 x 8192 tokens of 32 heads 93 us a call in a row of
+// calls, 0.59 of the copy peak. With a cold L2, the events' own 5 us in them: that call 99
+// us; 2047 tokens of 64 heads, half of the channels rotated, 24; 3 x 1601 tokens of 8
+// heads with three axes and the Hadamard rotation 15; one token of 32 sequences and 32 heads 9.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

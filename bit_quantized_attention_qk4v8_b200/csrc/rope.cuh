@@ -378,9 +378,9 @@ __device__ __forceinline__ void mxfp4_row8(const uint32_t (&w0)[4], const uint32
 
 // How a warp takes rows: TS tokens by HS heads at a time (TS * HS = 4), `heads` heads
 // (a multiple of HS) of its tokens in all, so that a token's cosines and sines
-// are read once for them. With 32 heads or more, one token by four heads: 8 steps use its
-// cosines up, and the table is read once for 32 rows (96 us for 32768 tokens of 32
-// heads; four tokens by one head: 99). With fewer, four tokens by one head, so that a lane's
+// are read once for them. (Times here are kernel durations in a profiler's trace.) With 32
+// heads or more, one token by four heads: 8 steps use its cosines up, and the table is
+// read once for 32 rows (96 us for 32768 tokens of 32 heads; four tokens by one head: 99). With fewer, four tokens by one head, so that a lane's
 // cosines still serve a head a step (8192 appended tokens of 8 heads, 4 sequences: 55 us;
 // one token by four heads: 64).
 struct RopeTiling {
@@ -399,7 +399,8 @@ inline RopeTiling rope_tiling(int B, int tokens, int H) {
     // Up to 8 steps over the heads an item, fewer while the items would not give every SM
     // 16 warps, two thirds of what it holds: with 32 asked for, an item's start (position, then
     // cosines) is paid in two waves of short items (3 x 1601 tokens of 8 heads 13.8 us,
-    // here 11.6), with 8 too few warps hide each other's (13.6).
+    // here 11.6), with 8 too few warps hide each other's (13.6). (2047 tokens of 64 heads, half of
+    // the channels rotated, pay for it: 18.7 us with 32, here 19.2.)
     int steps = 8;
     auto chunks = [&](int s) { return (H + s * hs - 1) / (s * hs); };
     while (steps > 1 && static_cast<int64_t>(B) * t.token_groups * chunks(steps) < 148 * 16) steps >>= 1;
